@@ -555,7 +555,9 @@ __device__ __forceinline__ float prefill_lay_out(int q, uint32_t sbase, const Pa
 #pragma unroll
   for (int i = 0; i < A::ACCESSES; ++i) {
     const uint32_t u[4] = {in.v[i].x, in.v[i].y, in.v[i].z, in.v[i].w};
-    const float down = __uint_as_float(static_cast<unsigned>(127 - exponent(top[i])) << 23) * 0x1p7f;
+    // a row with an infinity or NaN is NaN throughout, so that every score of it is, and a masked one stays masked
+    const float down =
+        top[i] >= 0x7f80u ? NAN : __uint_as_float(static_cast<unsigned>(127 - exponent(top[i])) << 23) * 0x1p7f;
     uint32_t hi[2], lo[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
@@ -576,9 +578,7 @@ __device__ __forceinline__ float prefill_lay_out(int q, uint32_t sbase, const Pa
     sts64(at, hi[0], hi[1]);
     sts64(at + S::Q_PART, lo[0], lo[1]);
   }
-  // an infinity or NaN in the row: every score of it; otherwise above 0, as the K scales are kept (a masked -inf stays
-  // one at scale 0)
-  if (mine >= 0x7f80u) return NAN;
+  // above 0, as the K scales are kept: a masked -inf stays one at scale 0
   return fmaxf(__uint_as_float(static_cast<unsigned>(127 + exponent(mine)) << 23) * 0x1p-7f * p.scale_log2, 0x1p-60f);
 }
 
@@ -632,7 +632,9 @@ __device__ __forceinline__ float prefill_lay_out_loop(int q, uint32_t sbase, con
 #pragma unroll
     for (int k = 0; k < G; ++k) {
       const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-      const float down = __uint_as_float(static_cast<unsigned>(127 - exponent(top[k])) << 23) * 0x1p7f;
+      // (NaN throughout where there is an infinity or NaN, as prefill_lay_out)
+      const float down =
+          top[k] >= 0x7f80u ? NAN : __uint_as_float(static_cast<unsigned>(127 - exponent(top[k])) << 23) * 0x1p7f;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float x[4];
@@ -656,9 +658,7 @@ __device__ __forceinline__ float prefill_lay_out_loop(int q, uint32_t sbase, con
       sts64(at + S::Q_PART, lo[k][0], lo[k][1]);
     }
   }
-  // an infinity or NaN in the row: every score of it; otherwise above 0, as the K scales are kept (a masked -inf stays
-  // one at scale 0)
-  if (mine >= 0x7f80u) return NAN;
+  // above 0, as the K scales are kept: a masked -inf stays one at scale 0
   return fmaxf(__uint_as_float(static_cast<unsigned>(127 + exponent(mine)) << 23) * 0x1p-7f * p.scale_log2, 0x1p-60f);
 }
 

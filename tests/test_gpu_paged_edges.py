@@ -1,0 +1,38 @@
+"""Attention over the paged e4m3 cache where its arithmetic is at an edge, against
+the 64-bit definition: queries that are not numbers, factors of any size, rows of Q
+whose elements differ much."""
+import math
+
+import pytest
+import torch
+
+import exact_attention_51_gb300 as ea
+from test_gpu_paged import assert_close, case, clean_status, on_gpu, reference  # noqa: F401  (a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [3, 70])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+def test_rows_without_keys_are_empty_whatever_their_query(new, d, value):
+    """More causal queries than keys: the first see none, and give O = 0 and LSE = -inf
+    even where their Q is not a number, among rows that see keys."""
+    c = case([new - 1], [new], 4, 2, d, 16, seed=60)
+    want = reference(c)
+    dev = on_gpu(c)
+    dev["q"][0, :3, 5] = value
+    for splits in (1, 2, 9):
+        assert_close(ea.attn_fwd_fp8_paged(**dev, max_q=new, max_kv=128, num_splits=splits), want)
+
+
+@pytest.mark.parametrize("new", [3, 70])
+def test_rows_whose_pages_are_all_hidden_are_empty_whatever_their_query(new):
+    c = case([new], [new], 4, 2, 64, 128, seed=61)
+    dev = on_gpu(c)
+    dev["q"][:] = math.nan
+    dev["block_table"][0, 0] = -5
+    for splits in (1, 2):
+        o, lse = ea.attn_fwd_fp8_paged(**dev, max_q=new, max_kv=256, num_splits=splits)
+        assert ea.attn_fwd_device_status() == (ea.ATTN_ERR_BAD_INDEX, 0x202)
+        assert o.eq(0).all() and lse.eq(-math.inf).all()
