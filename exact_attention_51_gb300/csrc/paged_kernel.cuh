@@ -232,6 +232,10 @@ __device__ __forceinline__ uint32_t split_nan(uint32_t x, uint32_t& nan) {
   return keep;
 }
 
+// What a block's scores are multiplied by: its K scale (2^-60 at least) times the row's factor, which may be 0.  The
+// smallest normal number on top, which others round away, keeps a masked -inf one however small they are.
+__device__ __forceinline__ float score_factor(float k_scale, float row) { return fmaf(k_scale, row, 0x1p-126f); }
+
 constexpr float kPagedGrow = 8.f;   // the offset moves when a term is past 2^8 of it
 // p' is kept 2^7 larger: below 2^15 in all, and normal in fp16 down to 2^-21 of the offset
 constexpr float kPagedShift = 7.f;
@@ -547,8 +551,7 @@ __global__ void __launch_bounds__(S::THREADS, S::MIN_BLOCKS)
           *reinterpret_cast<uint2*>(smem + S::OFF_Q + ((ks * NT + (n >> 3)) * 32 + (n & 7) * 4 + cc) * 8) = v;
         }
       }
-      // (above 0, as the K scales are kept: a masked -inf stays one at scale 0)
-      if (lane == 0) rowf[n] = fmaxf(up * p.scale_log2, 0x1p-60f);
+      if (lane == 0) rowf[n] = up * p.scale_log2;
     }
   }
   __syncthreads();
@@ -669,7 +672,7 @@ __global__ void __launch_bounds__(S::THREADS, S::MIN_BLOCKS)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            const float f0 = ksm[mt] * rf[nt][0], f1 = ksm[mt] * rf[nt][1];
+            const float f0 = score_factor(ksm[mt], rf[nt][0]), f1 = score_factor(ksm[mt], rf[nt][1]);
             x[mt][nt][0] = fmaf(s[mt][nt][0], f0, lv[mt] + base[nt][0]);
             x[mt][nt][1] = fmaf(s[mt][nt][1], f1, lv[mt] + base[nt][1]);
             x[mt][nt][2] = fmaf(s[mt][nt][2], f0, lv[mt] + base[nt][0]);
@@ -685,7 +688,7 @@ __global__ void __launch_bounds__(S::THREADS, S::MIN_BLOCKS)
               float y[MT][2];
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt) {
-                const float f = ksm[mt] * rf[nt][e];
+                const float f = score_factor(ksm[mt], rf[nt][e]);
                 y[mt][0] = fmaf(s[mt][nt][e], f, lv[mt]);
                 y[mt][1] = fmaf(s[mt][nt][e + 2], f, lv[mt]);
                 m = fmax3(m, y[mt][0], y[mt][1]);

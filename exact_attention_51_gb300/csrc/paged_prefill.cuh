@@ -448,7 +448,7 @@ __device__ __forceinline__ float prefill_exp(const uint32_t (&s)[NCH][32], float
     uint32_t pk[16];
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      const float a = (g ? lv.y : lv.x) - off, f = (g ? ks.y : ks.x) * rf;
+      const float a = (g ? lv.y : lv.x) - off, f = score_factor(g ? ks.y : ks.x, rf);
       const f32x2 ff = f2_pack(f, f), aa = f2_pack(a, a);
       f32x2 acc;
 #pragma unroll
@@ -481,7 +481,7 @@ __device__ __forceinline__ float prefill_max(const uint32_t (&s)[NCH][32], float
       b = fmax3(b, __uint_as_float(s[g / 2][(g & 1) * 16 + e + 2]), __uint_as_float(s[g / 2][(g & 1) * 16 + e + 3]));
     }
     a = fmax3(a, __uint_as_float(s[g / 2][(g & 1) * 16 + 14]), __uint_as_float(s[g / 2][(g & 1) * 16 + 15]));
-    m = fmaxf(m, fmaf(fmaxf(a, b), meta[8 + g] * rf, meta[16 + g]));
+    m = fmaxf(m, fmaf(fmaxf(a, b), score_factor(meta[8 + g], rf), meta[16 + g]));
   }
   return m;
 }
@@ -578,8 +578,7 @@ __device__ __forceinline__ float prefill_lay_out(int q, uint32_t sbase, const Pa
     sts64(at, hi[0], hi[1]);
     sts64(at + S::Q_PART, lo[0], lo[1]);
   }
-  // above 0, as the K scales are kept: a masked -inf stays one at scale 0
-  return fmaxf(__uint_as_float(static_cast<unsigned>(127 + exponent(mine)) << 23) * 0x1p-7f * p.scale_log2, 0x1p-60f);
+  return __uint_as_float(static_cast<unsigned>(127 + exponent(mine)) << 23) * 0x1p-7f * p.scale_log2;
 }
 
 // The same in a loop of four accesses, with the next four on their way, for d = 256: its 32
@@ -658,8 +657,7 @@ __device__ __forceinline__ float prefill_lay_out_loop(int q, uint32_t sbase, con
       sts64(at + S::Q_PART, lo[k][0], lo[k][1]);
     }
   }
-  // above 0, as the K scales are kept: a masked -inf stays one at scale 0
-  return fmaxf(__uint_as_float(static_cast<unsigned>(127 + exponent(mine)) << 23) * 0x1p-7f * p.scale_log2, 0x1p-60f);
+  return __uint_as_float(static_cast<unsigned>(127 + exponent(mine)) << 23) * 0x1p-7f * p.scale_log2;
 }
 
 // What a softmax thread has of its row once the last product is in tensor memory.

@@ -36,3 +36,18 @@ def test_rows_whose_pages_are_all_hidden_are_empty_whatever_their_query(new):
         o, lse = ea.attn_fwd_fp8_paged(**dev, max_q=new, max_kv=256, num_splits=splits)
         assert ea.attn_fwd_device_status() == (ea.ATTN_ERR_BAD_INDEX, 0x202)
         assert o.eq(0).all() and lse.eq(-math.inf).all()
+
+
+@pytest.mark.parametrize("new", [3, 70])
+@pytest.mark.parametrize("q,k,scale", [(1.0, 2.0 ** 60, 0.0), (2.0 ** -100, 2.0 ** 60, 0.125),
+                                       (1.0, 2.0 ** -60, 2.0 ** 60), (1.0, 2.0 ** -60, 0.0)])
+def test_score_factors_of_any_size(new, q, k, scale):
+    """Small factors of Q and the scale against large keys, and the other way round: no
+    factor is held at a bound of its own, and a masked key stays one however small they are."""
+    c = case([200, 90], [1, new], 4, 2, 64, 16, seed=62, spread=0)
+    c["q"] = (c["q"].double() * q).to(torch.bfloat16)
+    c["ks"] = torch.full_like(c["ks"], k)
+    want = reference(c, scale=scale)
+    dev = on_gpu(c)
+    for splits in (1, 2, 9):
+        assert_close(ea.attn_fwd_fp8_paged(**dev, max_q=new, max_kv=200, scale=scale, num_splits=splits), want)
