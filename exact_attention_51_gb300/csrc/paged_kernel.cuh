@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(S::THREADS, S::MIN_BLOCKS)
       nan = __any_sync(0xffffffffu, nan);
       int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
       if (nan) ex = 0;
-      ex = max(ex, -100);  // (a row of zeros or subnormals)
+      ex = max(ex, -126);  // (a row of zeros or subnormals, which have fewer digits)
       const float down = __uint_as_float(static_cast<unsigned>(127 - min(ex, 126)) << 23);
       const float up = __uint_as_float(static_cast<unsigned>(127 + min(ex, 126)) << 23);
 #pragma unroll

@@ -549,8 +549,9 @@ __device__ __forceinline__ float prefill_lay_out(int q, uint32_t sbase, const Pa
     const uint32_t other = __shfl_sync(0xffffffffu, top[i], lane % A::ROWS * A::LANES);
     if (lane / A::ROWS == i) mine = other;
   }
+  // (down to -120, so that 2^7 times its reciprocal is a number; the bits of subnormals are all in range)
   auto exponent = [](uint32_t bits) {
-    return bits >= 0x7f80u ? 0 : max(min(static_cast<int>(bits >> 7) - 127, 126), -100);
+    return bits >= 0x7f80u ? 0 : max(min(static_cast<int>(bits >> 7) - 127, 126), -120);
   };
 #pragma unroll
   for (int i = 0; i < A::ACCESSES; ++i) {
@@ -602,7 +603,7 @@ __device__ __forceinline__ float prefill_lay_out_loop(int q, uint32_t sbase, con
     }
   };
   auto exponent = [](uint32_t bits) {
-    return bits >= 0x7f80u ? 0 : max(min(static_cast<int>(bits >> 7) - 127, 126), -100);
+    return bits >= 0x7f80u ? 0 : max(min(static_cast<int>(bits >> 7) - 127, 126), -120);
   };
   uint32_t mine = 0;  // this thread's row's largest
   fetch(0);

@@ -51,3 +51,17 @@ def test_score_factors_of_any_size(new, q, k, scale):
     dev = on_gpu(c)
     for splits in (1, 2, 9):
         assert_close(ea.attn_fwd_fp8_paged(**dev, max_q=new, max_kv=200, scale=scale, num_splits=splits), want)
+
+
+@pytest.mark.parametrize("new", [3, 70])
+@pytest.mark.parametrize("q", [2.0 ** -110, 2.0 ** -124, 2.0 ** -131, 2.0 ** 126])
+def test_rows_of_q_at_the_ends_of_bf16(new, q):
+    """As exact as other rows, subnormal ones too (whose few digits bf16 has rounded already)."""
+    c = case([200, 90], [1, new], 4, 2, 64, 16, seed=64, spread=0)
+    c["q"] = (c["q"].double().clamp(-1.9, 1.9) * q).to(torch.bfloat16)
+    c["ks"] = torch.full_like(c["ks"], 2.0 ** 40 if q < 1 else 2.0 ** -60)
+    scale = 2.0 ** -10 / q * (2.0 ** -40 if q < 1 else 2.0 ** 60)
+    want = reference(c, scale=scale)
+    dev = on_gpu(c)
+    for splits in (1, 2, 9):
+        assert_close(ea.attn_fwd_fp8_paged(**dev, max_q=new, max_kv=200, scale=scale, num_splits=splits), want)
