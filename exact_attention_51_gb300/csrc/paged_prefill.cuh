@@ -13,10 +13,12 @@
 //   softmax       one warpgroup a tile, one thread a row, as attn_fwd_kernel; the first
 //                 thing it does is to lay out its Q rows.
 //
-// K is multiplied as it is stored (kind::f8f6f4): a row of Q, scaled by a power of two,
-// is the sum of two e4m3 rows, each of which takes four of bf16's eight digits, and the two
-// products cost what one of 16 bits does.  (Where an element is so small that the second part
-// leaves e4m3's range, it is off by at most 2^-18 of the row's largest.)  P has no such range -- a flat tail
+// K is multiplied as it is stored (kind::f8f6f4): a row of Q, its largest element brought to [2^7, 2^8) by a
+// power of two, is the sum of an e4m3 row and an e5m2 row, and the two products cost what one of 16 bits does.
+// e4m3 takes the upper four of bf16's eight digits; what rounding to them leaves is at most 8 of bf16's steps, which
+// e5m2's three digits hold.  So elements of 2^-6 and more are exact (2^-14 of the row's largest).  Below, e4m3's
+// step is 2^-9 and leaves up to 2^-10, where e5m2's is 2^-13: off by 2^-14 at most, 2^-21 of the row's largest.
+// (With e4m3 for the second part as well, its range would end 2^-17 below.)  P has no such range -- a flat tail
 // behind one heavy key is 2^-20 of it -- so P V is fp16 and V is converted: K's
 // conversion would cost as much again of the shared memory's time.
 //
@@ -130,6 +132,9 @@ struct PrefillTile {
   int t_end;          // keys from here on are not this block's
   int lim_min;        // keys that every row of the block sees
 };
+
+// kind::f8f6f4 descriptor with e5m2 A (format 1) and e4m3 B, both K-major, and fp32 accumulate.
+__host__ __device__ constexpr uint32_t idesc_e5m2_e4m3_f32(int M, int N) { return idesc_e4m3_f32(M, N) | (1u << 7); }
 
 // kind::f16 descriptor with fp16 A and B (format 0) and fp32 accumulate.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major) {
@@ -328,7 +333,8 @@ __device__ void prefill_convert(const PagedParams& p, const PrefillTile<S>& t, u
 template <typename S>
 __device__ void prefill_mma(uint32_t tmem, uint32_t sbase, const PrefillTile<S>& t, Waiter w) {
   constexpr int NQ = S::NQ, NSB = S::NSB;
-  constexpr uint32_t kQK = idesc_e4m3_f32(BM, S::BN), kPV = idesc_f16_f32(BM, S::D, true);
+  constexpr uint32_t kQK[2] = {idesc_e4m3_f32(BM, S::BN), idesc_e5m2_e4m3_f32(BM, S::BN)};
+  constexpr uint32_t kPV = idesc_f16_f32(BM, S::D, true);
   const uint32_t bar0 = sbase + S::OFF_BAR;
   auto bar = [&](int i) { return bar0 + 8u * static_cast<uint32_t>(i); };
   const uint32_t leader = elect_one();
@@ -354,7 +360,7 @@ __device__ void prefill_mma(uint32_t tmem, uint32_t sbase, const PrefillTile<S>&
       for (int k = 0; k < S::KSTEPS_QK; ++k) {
         const uint32_t ao = ((k / KPP) * S::Q_PANEL + (k % KPP) * 32) >> 4;
         const uint32_t bo = ((k / KPP) * S::RAW_PANEL + (k % KPP) * 32) >> 4;
-        mma_ss_f8(tmem + S::s_col(q, b), a0 + ao, b0 + bo, kQK, part + k > 0 ? 1u : 0u, leader);
+        mma_ss_f8(tmem + S::s_col(q, b), a0 + ao, b0 + bo, part ? kQK[1] : kQK[0], part + k > 0 ? 1u : 0u, leader);
       }
     }
     mma_commit(bar(S::B_S + q * NSB + b), leader);
@@ -493,6 +499,18 @@ __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 
+// Four fp32 values to e5m2 codes, nearest (b0 the lowest byte).
+__device__ __forceinline__ uint32_t pack_e5m2x4(float b0, float b1, float b2, float b3) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e5m2x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(b0), "f"(b1), "f"(b2), "f"(b3));
+  return r;
+}
+
 template <typename S>
 struct PrefillRows {
   static constexpr int LANES = S::D / 8, ROWS = 32 / LANES, ACCESSES = LANES;
@@ -524,7 +542,7 @@ __device__ __forceinline__ void prefill_fetch(int q, const PagedParams& p, const
   }
 }
 
-// Lays out a warp's rows of Q, each with its largest element brought to [2^7, 2^8), as the sum of two e4m3 rows, and
+// Lays out a warp's rows of Q, each with its largest element brought to [2^7, 2^8), as an e4m3 and an e5m2 row, and
 // returns the factor of this thread's row's scores.
 template <typename S>
 __device__ __forceinline__ float prefill_lay_out(int q, uint32_t sbase, const PagedParams& p, const PrefillQ<S>& in) {
@@ -572,7 +590,7 @@ __device__ __forceinline__ float prefill_lay_out(int q, uint32_t sbase, const Pa
       const uint32_t h01 = e4m3_lo(hi[e]), h23 = e4m3_hi(hi[e]);
       const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
       const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
-      lo[e] = pack_e4m3x4(x[0] - f01.x, x[1] - f01.y, x[2] - f23.x, x[3] - f23.y);
+      lo[e] = pack_e5m2x4(x[0] - f01.x, x[1] - f01.y, x[2] - f23.x, x[3] - f23.y);
     }
     const int r = (threadIdx.x & 96) + i * A::ROWS + lane / A::LANES;
     const uint32_t at = paged_chunk<S::D, BM>(dst, r, lane % A::LANES / 2) + (lane & 1) * 8;
@@ -647,7 +665,7 @@ __device__ __forceinline__ float prefill_lay_out_loop(int q, uint32_t sbase, con
         const uint32_t h01 = e4m3_lo(hi[k][e]), h23 = e4m3_hi(hi[k][e]);
         const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&h01));
         const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&h23));
-        lo[k][e] = pack_e4m3x4(x[0] - f01.x, x[1] - f01.y, x[2] - f23.x, x[3] - f23.y);
+        lo[k][e] = pack_e5m2x4(x[0] - f01.x, x[1] - f01.y, x[2] - f23.x, x[3] - f23.y);
       }
     }
 #pragma unroll

@@ -65,3 +65,37 @@ def test_rows_of_q_at_the_ends_of_bf16(new, q):
     dev = on_gpu(c)
     for splits in (1, 2, 9):
         assert_close(ea.attn_fwd_fp8_paged(**dev, max_q=new, max_kv=200, scale=scale, num_splits=splits), want)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("new", [4, 5, 70])
+def test_rows_of_q_with_one_large_element(new, d):
+    """One channel of Q is 2^12 to 2^17 times the rest, and the keys have nothing in it, so
+    that the scores are those of the small elements alone.
+
+    Sixteen rows and fewer hold Q in fp16, exact here.  More rows hold it as an e4m3 and
+    an e5m2 part.  A row's largest element is at 2^7 at least.  What the e4m3 part leaves of an element of 2^-6 or
+    more is at most 8 steps of bf16: 3 digits, which e5m2 has.  Of a smaller one it leaves at most 2^-10, where
+    e5m2's steps are 2^-13: off by 2^-14 at most, 2^-21 of the row's largest."""
+    g = torch.Generator().manual_seed(63)
+    c = case([90], [new], 4, 1, d, 16, seed=63, spread=0)
+    small = torch.tensor([2.0 ** -5, 2.0 ** -7, 2.0 ** -9, 2.0 ** -11, -2.0 ** -10, 2.0 ** -11])  # (the last: all alike)
+    rows = torch.arange(new * 4).view(new, 4)
+    c["q"] = (small[rows % 6][..., None] * (1 + torch.rand((new, 4, d), generator=g))).to(torch.bfloat16)
+    c["q"][rows % 6 == 5] = 2.0 ** -11
+    c["q"][..., 0] = 64.0
+    keys = (0.25 + torch.rand((c["kc"].shape[0], 1, 16, d), generator=g)) * torch.rand((c["kc"].shape[0], 1, 16, 1), generator=g)
+    keys[..., 0] = 0
+    c["kc"] = keys.to(torch.float8_e4m3fn)
+    c["ks"] = torch.ones_like(c["ks"])
+    scale = 8.0
+    o, lse, tol_o, tol_l = reference(c, scale=scale)
+    if new * 4 > 16:
+        # a weight carries its score's error, and so does the normaliser; sum w |v| is below the largest |v|
+        seen = torch.cat([c["kc"][int(p), 0].double() for p in c["table"][0, :6]])[:90]
+        e = 2.0 ** -21 * 64 * seen.abs().sum(-1).max() * scale
+        values = torch.cat([c["vc"][int(p), 0].double() * c["vs"][int(p), 0] for p in c["table"][0, :6]])[:90]
+        tol_o, tol_l = tol_o + 2 * e * values.abs().max(), tol_l + 2 * e
+    dev = on_gpu(c)
+    for splits in (1, 2, 9):
+        assert_close(ea.attn_fwd_fp8_paged(**dev, max_q=new, max_kv=90, scale=scale, num_splits=splits), (o, lse, tol_o, tol_l))
