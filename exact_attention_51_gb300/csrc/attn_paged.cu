@@ -197,12 +197,13 @@ int attn_fwd_fp8_paged_num_splits(int B, int Hq, int Hkv, int d, int page_size, 
     double t;
     if (long_tile) {
       // A turn of the tcgen05 kernel takes 1.75 us at each head dim, to begin and end a block 10, the merge in a cluster
-      // 6; clusters of 3 and 4 leave multiprocessors empty.  Measured over nine shapes (64 to 4096
+      // 6; clusters of 3 and 4 leave multiprocessors empty, and a last wave in halves takes half a wave.  Measured
+      // over nine shapes (64 to 4096
       // queries of 8192 to 32768 keys), the count taken was the fastest or within 2 % of it.
       const bool cluster = s > 1 && s <= kPrefillCluster;
       double queue = per_sm <= 1.0 ? 1.0 : 0.5 * (std::ceil(per_sm) + per_sm) * (cluster && s > 2 ? 1.08 : 1.0);
-      const PagedTail tail = paged_tail(static_cast<long long>(ctas), num_sms, max_q, max_kv, true);
-      if (s == 1 && tail.splits > 1) queue = std::min(queue, std::floor(per_sm) + 1.1 / tail.splits);
+      if (s == 1 && paged_tail(static_cast<long long>(ctas), num_sms, max_q, max_kv, true) > 0)
+        queue = std::min(queue, std::floor(per_sm) + 0.5);
       t = 4.0 + queue * (turns * 1.75 + 10.0 + (cluster ? 6.0 : 0.0)) + (s > kPrefillCluster ? 3.0 + partial * s : 0.0);
     } else {
       // Clusters want all their blocks at once (B=64 up to 16384 keys, 32/8 heads: 165 us in clusters of 4 to 8, 133 with
@@ -323,10 +324,8 @@ int attn_fwd_fp8_paged(const void* q, int64_t q_stride_t, int64_t q_stride_h, co
   p.splits = num_splits;
   p.cluster = cluster;
   p.shares = num_splits / cluster;
-  if (tile_rows >= kPrefillRows && num_splits == 1) {
-    const PagedTail tail = paged_tail(tiles * Hkv * B, sms, max_q, max_kv, causal != 0);
-    if (tail.splits > 1) p.first_tile = static_cast<int>(tail.first), p.tail_splits = tail.splits;
-  }
+  if (tile_rows >= kPrefillRows && num_splits == 1)
+    p.tail_tile = static_cast<int>(paged_tail(tiles * Hkv * B, sms, max_q, max_kv, causal != 0));
   const long long units = (static_cast<long long>(max_kv) + kPagedUnit - 1) / kPagedUnit;
   p.chunk = static_cast<int>(std::min<long long>((units + num_splits - 1) / num_splits * kPagedUnit, 1LL << 30));
   p.causal = causal != 0;

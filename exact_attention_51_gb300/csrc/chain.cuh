@@ -7,7 +7,7 @@
 // wait (chain_begin) until it has completed and its writes can be seen.
 //
 // Every thread of every block of a kernel launched this way calls chain_begin
-// before it reads or writes global memory or leaves (or chain_join and chain_end): so a kernel completes only
+// before it reads or writes global memory or leaves: so a kernel completes only
 // after all that were launched before it, and what follows it, launched either
 // way, sees their results.
 #pragma once
@@ -23,12 +23,6 @@ __device__ __forceinline__ void chain_begin() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
-
-// For the second of two launches that do not need each other's results: its blocks run as soon as the first one's
-// have all begun, which is after everything before that one, and wait for the first one's end with chain_end before
-// they leave.
-__device__ __forceinline__ void chain_join() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void chain_end() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // kern<<<grid, block, smem, stream>>>(args...) with blocks placed early, in clusters of
 // `cluster` along x.

@@ -31,8 +31,7 @@ struct PagedParams {
   int splits, chunk;  // keys a split takes (the last one takes all that is left)
   int cluster;        // splits that a thread-block cluster merges in shared memory
   int shares;         // splits / cluster: partial results that the merge kernel joins
-  int first_tile;     // tcgen05 kernel: row tiles from here on are this launch's (> 0: it joins the launch before it)
-  int tail_splits;    // shares of the keys of those, the last wave's; 0: one launch
+  int tail_tile;      // tcgen05 kernel: row tiles from here on, the last wave's, are a cluster's of two; 0: none
   int causal;
   float scale_log2;  // scale * log2(e)
 };
@@ -60,24 +59,17 @@ constexpr int paged_blocks(int d, int tile_rows, int page_size) {
 // fill a group of multiprocessors.
 constexpr int kPrefillCluster = 4;
 
-// Row tiles of the tcgen05 kernel that the last, partial wave is left with where its blocks take whole tiles, and the
-// shares that their keys are cut in to fill it: 2 x 2048 queries against 16384 keys are 512 tiles, three waves
-// of 152 and 56 that two blocks each take (836 us, 899 without).  Where the tiles' keys differ much, as in a whole
-// prompt, the longest come first and the short ones fill the gaps already (4096 against 4096: 134 us, 145 in
-// two launches).
-struct PagedTail {
-  long long first;  // 0: all tiles alike
-  int splits;
-};
-inline PagedTail paged_tail(long long tiles, int num_sms, long long max_q, long long max_kv, bool causal) {
-  const long long first = tiles / num_sms * num_sms, rest = tiles - first;
-  // (below 2048 keys a share's begin, end and merge cost what it saves; larger clusters do not fill the groups of
-  // multiprocessors)
-  if (first == 0 || rest == 0 || 2 * rest > num_sms || max_kv < 2048) return {0, 1};
-  if (causal && 4 * max_q > max_kv) return {0, 1};
-  int splits = 2;
-  while (splits < kPrefillCluster && (splits + 1) * rest * 10 <= 9LL * num_sms) ++splits;
-  return {first, splits};
+// First of the row tiles of the tcgen05 kernel that are left for a last, partial wave where blocks take whole tiles (0:
+// all tiles alike).  Two blocks of a cluster share such a tile's keys: 2 x 2048 queries against 16384 keys
+// are 512 tiles, three waves of 152 and 56 that two blocks each take (823 us, 911 without; 192 tiles at d = 64 293 and 367).  The launch is one of clusters
+// of two, and those before take two tiles each: 152 multiprocessors hold 76 of them.  (Of four they would leave some
+// empty in every wave.)  Where the tiles' keys differ much, as in a whole prompt, the longest come first and the short
+// ones fill the gaps already (4096 against 4096: 134 us, 145 in this way).
+inline long long paged_tail(long long tiles, int num_sms, long long max_q, long long max_kv, bool causal) {
+  const long long first = tiles / num_sms * num_sms / 2 * 2, rest = tiles - first;
+  // (below 2048 keys a share's begin, end and merge cost what it saves)
+  if (first == 0 || rest == 0 || 2 * rest > num_sms || max_kv < 2048) return 0;
+  return causal && 4 * max_q > max_kv ? 0 : first;
 }
 
 // Splits that a cluster takes: all or one.

@@ -42,20 +42,12 @@ cudaError_t launch_prefill(const CUtensorMap* tk, const CUtensorMap* tv, const P
   using S = PrefillShape<D>;
   static std::atomic<unsigned long long> configured{0};
   auto kern = paged_prefill_kernel<S>;
-  cudaError_t e = paged_configure(kern, S::SMEM_ALLOC, configured);
+  const cudaError_t e = paged_configure(kern, S::SMEM_ALLOC, configured);
   if (e != cudaSuccess) return e;
   const unsigned tiles = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.tiles) * static_cast<unsigned>(p.Hkv);
-  if (p.tail_splits > 1) {  // the last wave's tiles in a launch of their own
-    PagedParams tail = p;
-    tail.splits = tail.cluster = p.tail_splits;
-    const unsigned rest = tiles - static_cast<unsigned>(p.first_tile);
-    PagedParams full = p;
-    full.first_tile = 0;
-    e = chain_launch(kern, static_cast<unsigned>(p.first_tile), S::THREADS, S::SMEM_ALLOC, stream, 1, *tk, *tv, full);
-    if (e != cudaSuccess) return e;
-    return chain_launch(kern, rest * static_cast<unsigned>(tail.splits), S::THREADS, S::SMEM_ALLOC, stream,
-                        static_cast<unsigned>(tail.cluster), *tk, *tv, tail);
-  }
+  if (p.tail_tile > 0)  // the last wave's tiles take two blocks each
+    return chain_launch(kern, 2 * tiles - static_cast<unsigned>(p.tail_tile), S::THREADS, S::SMEM_ALLOC, stream, 2, *tk,
+                        *tv, p);
   return chain_launch(kern, tiles * static_cast<unsigned>(p.splits), S::THREADS, S::SMEM_ALLOC, stream,
                       static_cast<unsigned>(p.cluster), *tk, *tv, p);
 }

@@ -124,7 +124,9 @@ struct PrefillShape {
 template <typename S>
 struct PrefillTile {
   PagedSeq seq;
-  int h, b, split;
+  int h, b;
+  int split, splits;  // which of the shares of the keys
+  int cluster;        // blocks of the cluster that share this tile (1: none do, or by way of the workspace)
   int row0, rows;     // first row of the block, rows of the sequence and key head
   int lo;             // first key tile
   int nkv[S::NQ];     // key tiles [lo, lo + nkv) of each row tile
@@ -145,8 +147,16 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
 template <typename S>
 __device__ __forceinline__ bool prefill_tile(const PagedParams& p, PrefillTile<S>& t, bool report) {
   int cta = static_cast<int>(blockIdx.x);
-  t.split = cta % p.splits;
-  cta = cta / p.splits + p.first_tile;
+  if (p.tail_tile > 0) {  // (one split: the last wave's tiles are shared by two blocks)
+    const int past = cta - p.tail_tile;
+    t.splits = t.cluster = past < 0 ? 1 : 2;
+    t.split = past < 0 ? 0 : past & 1;
+    if (past >= 0) cta = p.tail_tile + (past >> 1);
+  } else {
+    t.splits = p.splits, t.cluster = p.cluster;
+    t.split = cta % p.splits;
+    cta /= p.splits;
+  }
   t.h = cta % p.Hkv;
   cta /= p.Hkv;
   t.b = cta % p.B;
@@ -160,10 +170,10 @@ __device__ __forceinline__ bool prefill_tile(const PagedParams& p, PrefillTile<S
   t.lim_min = paged_limit(p, t.seq, t.row0 / p.group);
   // A cluster's blocks hold a multiprocessor each until its last one is done: they share out the keys that these rows
   // see.  (Shares of a workspace are the same for all rows.)
-  const int chunk = p.cluster > 1 ? max(1, (lim_max + S::BN * p.cluster - 1) / (S::BN * p.cluster)) * S::BN : p.chunk;
+  const int chunk = t.cluster > 1 ? max(1, (lim_max + S::BN * t.cluster - 1) / (S::BN * t.cluster)) * S::BN : p.chunk;
   const long long first = static_cast<long long>(t.split) * chunk;
   const int t_begin = static_cast<int>(min(first, static_cast<long long>(lim_max)));
-  t.t_end = t.split == p.splits - 1 ? lim_max : static_cast<int>(min(first + chunk, static_cast<long long>(lim_max)));
+  t.t_end = t.split == t.splits - 1 ? lim_max : static_cast<int>(min(first + chunk, static_cast<long long>(lim_max)));
   t.lo = t_begin / S::BN;  // a multiple of BN, or past every key
   t.n = 0;
 #pragma unroll
@@ -886,13 +896,9 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_addr(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (p.first_tile > 0) chain_join();
-  else chain_begin();
+  chain_begin();
   PrefillTile<S> t;
-  if (!prefill_tile<S>(p, t, threadIdx.x == 0)) {
-    if (p.first_tile > 0) chain_end();
-    return;
-  }
+  if (!prefill_tile<S>(p, t, threadIdx.x == 0)) return;
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + S::OFF_ABORT);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::OFF_TMEMSLOT);
   const Waiter w{abort_flag, p.status};
@@ -931,15 +937,15 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     if constexpr (S::D == 128) prefill_fetch<S>(q, p, t, rows);
     const PrefillRow<S> row = prefill_softmax<S>(q, tmem, smem, sbase, tile, p, rows, w);
     tc_fence_after_sync();
-    if (p.cluster == 1 && (row.has || tile.nkv[q] == 0))  // (not if a wait gave up)
+    if (tile.cluster == 1 && (row.has || tile.nkv[q] == 0))  // (not if a wait gave up)
       prefill_store<S>(q, tmem, sbase, tile, p, row);
     tc_fence_before_sync();
     __syncthreads();
-    if (p.cluster > 1) {
+    if (tile.cluster > 1) {
       tc_fence_after_sync();
       prefill_offer<S>(q, tmem, smem, row);
       tc_fence_before_sync();
-      paged_cluster_merge<S>(p, smem, sbase, 0, tile.split, p.cluster, min(S::ROWS, tile.rows - tile.row0),
+      paged_cluster_merge<S>(p, smem, sbase, 0, tile.split, tile.cluster, min(S::ROWS, tile.rows - tile.row0),
                              static_cast<long long>(p.T) * p.Hq, [&](int n) { return prefill_place<S>(p, tile, n); });
     }
   } else {
@@ -959,13 +965,12 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     __syncwarp();
     tc_fence_before_sync();
     __syncthreads();
-    if (p.cluster > 1) cluster_arrive(), cluster_wait(), cluster_arrive(), cluster_wait();  // as paged_cluster_merge
+    if (t.cluster > 1) cluster_arrive(), cluster_wait(), cluster_arrive(), cluster_wait();  // as paged_cluster_merge
     if (warp == S::MMA_WARP) {
       tc_fence_after_sync();
       tmem_dealloc(tmem, S::TMEM_COLS);
     }
   }
-  if (p.first_tile > 0) chain_end();
 }
 
 }  // namespace ea51

@@ -110,7 +110,7 @@ ATTN_API int attn_paged_append_fp8(const void* k, const void* v, int T, int Hkv,
  * Page numbers outside of [0, num_pages) and lengths beyond the table hide their tokens and set
  * 0x202 in the status word; sequence starts out of order or beyond T hide the
  * sequence, and more than max_q query tokens are left out, with 0x203.
- * Enqueues one kernel (or two: the last wave's blocks), and a merge where there is a workspace.  Up to 16 rows
+ * Enqueues one kernel, and a merge where there is a workspace.  Up to 16 rows
  * (max_q * Hq / Hkv) of a sequence and key head run a kernel that reads the keys
  * once for all of them (its grid takes at most 65535 sequences and 65535 key
  * heads), more run on the tcgen05 tensor cores.

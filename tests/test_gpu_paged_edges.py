@@ -99,3 +99,48 @@ def test_rows_of_q_with_one_large_element(new, d):
     dev = on_gpu(c)
     for splits in (1, 2, 9):
         assert_close(ea.attn_fwd_fp8_paged(**dev, max_q=new, max_kv=90, scale=scale, num_splits=splits), (o, lse, tol_o, tol_l))
+
+
+@pytest.mark.parametrize("d,tokens", [(64, 270), (128, 270), (256, 134)])
+def test_last_wave_sees_what_was_written_right_before(d, tokens):
+    """A wave of blocks and a few more, whose keys pairs of blocks share: lengths, page
+    numbers, queries and the cache are written by the launches right before, without a wait, and read
+    as after one."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    B = -(-(sms + 9) // 5)  # two tiles of each of three heads: a wave and a fifth
+    g = torch.Generator().manual_seed(65)
+    c = case([2048 + 16 * (b % 5) for b in range(B)], [tokens] * B, 3, 3, d, 128, seed=65)
+    dev = on_gpu(c)
+    pages = c["kc"].shape[0]
+    dev["block_table"] = torch.cat([dev["block_table"].clamp(min=0), dev["block_table"].clamp(min=0)[:, :1]], 1).contiguous()
+    tables = [dev["block_table"].clone(), dev["block_table"].flip(0).contiguous()]
+    lens = [dev["kv_len"].clone(), dev["kv_len"].flip(0).contiguous()]
+    kv = torch.randn((6, 2, 8, 3, d), generator=g).to(torch.bfloat16).cuda()
+    start = [dev[k].clone() for k in ("q", "k_cache", "v_cache", "k_scale", "v_scale")]
+
+    def run(wait):
+        sync = torch.cuda.synchronize if wait else lambda: None
+        for k, t in zip(("q", "k_cache", "v_cache", "k_scale", "v_scale"), start):
+            dev[k].view(torch.uint8).copy_(t.view(torch.uint8))
+        got = []
+        for i in range(6):
+            # eight tokens over the beginning of a page that some sequence has
+            slots = (i * 7 % pages) * 128 + torch.arange(8, dtype=torch.int32, device="cuda")
+            dev["q"].mul_(-1.25)
+            dev["block_table"].copy_(tables[i % 2])
+            dev["kv_len"].copy_(lens[i % 2])
+            sync()
+            ea.attn_paged_append_fp8(kv[i, 0], kv[i, 1], slots, dev["k_cache"], dev["v_cache"], dev["k_scale"], dev["v_scale"])
+            sync()
+            got += ea.attn_fwd_fp8_paged(**dev, max_q=tokens, max_kv=2112, num_splits=1)
+            sync()
+            dev["kv_len"].zero_()
+            dev["block_table"].zero_()
+            sync()
+        return got
+
+    want = run(True)
+    assert not torch.equal(want[0], want[2])
+    for _ in range(3):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a.isnan(), b.isnan()) and torch.equal(a.nan_to_num(), b.nan_to_num())
