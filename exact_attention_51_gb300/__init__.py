@@ -600,7 +600,9 @@ def attn_rope(x, phases, positions=None, position0: int = 0, interleaved: bool =
     (i, i + rot_dim / 2), or (2i, 2i + 1) with ``interleaved`` -- by the angle of
     the token's position: ``positions`` int32 [N] or [B, N], or ``position0 + n``.
     ``phases`` and ``attention_factor`` as from ``attn_rope_phases``.  ``out``
-    may be ``x`` (in place).  Returns ``out``.  Like the other calls it records no
+    may be ``x`` (in place).  Returns ``out``.  With ``stream`` the call runs there,
+    behind what that stream has; the caller puts the inputs before and the
+    result's use after.  Like the other calls it records no
     autograd graph; ``attn_rope_bwd`` is its gradient."""
     return (_fast or _load_binding()).rope(False, x, phases, positions, position0, interleaved,
                                            attention_factor, out, stream)
@@ -666,7 +668,7 @@ def attn_fwd_fp8_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_le
     -inf, and rows of tokens that no sequence has are left as they were.
     ``num_splits`` None picks a count; the workspace it needs is allocated
     with torch unless given, and is scratch until the call has run: calls that may
-    overlap need one each."""
+    overlap need one each.  ``stream`` as in ``attn_rope``."""
     return (_fast or _load_binding()).paged(q, k_cache, v_cache, k_scale, v_scale, block_table,
                                                kv_len, q_start, max_q, max_kv, causal, scale,
                                                num_splits, out, lse, workspace, stream)

@@ -73,13 +73,17 @@ bool truth(PyObject* o) {
 }
 
 // The stream of a call: the given one, or torch's current one on the device.
+//
+// What the call allocates is of the call's stream: torch's allocator hands out a freed block again in the order of
+// the stream that it is of, so that on any other one the kernels before could still be using it.
 struct Stream {
   void* handle;
+  c10::cuda::CUDAStream current;  // the caller's
   std::optional<c10::cuda::CUDAStream> given;
 
-  Stream(PyObject* o, c10::DeviceIndex device) {
+  Stream(PyObject* o, c10::DeviceIndex device) : current(c10::cuda::getCurrentCUDAStream(device)) {
     if (o == Py_None) {
-      handle = c10::cuda::getCurrentCUDAStream(device).stream();
+      handle = current.stream();
       return;
     }
     unsigned long long bits;
@@ -96,9 +100,17 @@ struct Stream {
     given = c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), device);
   }
 
-  // Tells torch's allocator that the call's stream uses `t`, which was allocated on the current one.
-  void uses(const at::Tensor& t) const {
-    if (given) t.record_stream(given->unwrap());
+  // make() with the call's stream as torch's current one.
+  template <typename F>
+  at::Tensor alloc(F&& make) const {
+    if (!given) return make();
+    const c10::cuda::CUDAStreamGuard on(*given);
+    return make();
+  }
+
+  // Tells torch's allocator that the caller, who gets `t`, uses it on a stream of its own.
+  void returns(const at::Tensor& t) const {
+    if (given && *given != current) t.record_stream(current.unwrap());
   }
 };
 
@@ -196,23 +208,23 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bool interleaved = truth(a[5]);
     const float factor = static_cast<float>(number(a[6]));
     const c10::cuda::OptionalCUDAGuard guard(device);
+    const Stream stream(a[8], device.index());
     at::Tensor y;
     const bool made = a[7] == Py_None;
     if (made) {
-      y = new_like(x);
+      y = stream.alloc([&] { return new_like(x); });
     } else {
       y = must_be_tensor(a[7], "out");
       check(y.sizes() == x.sizes() && y.scalar_type() == type && y.device() == device && (y.stride(3) == 1 || d == 1),
             "out must be shaped and typed like x on its device, with the elements of a head adjacent");
     }
     if (x.numel() > 0) {
-      const Stream stream(a[8], device.index());
       const auto xs = x.strides(), ys = y.strides();
       const int rc = (backward ? attn_rope_bwd : attn_rope)(
           x.data_ptr(), y.data_ptr(), dtype, B, H, N, d, xs[0], xs[1], xs[2], ys[0], ys[1], ys[2], pos, stride_b, position0, u,
           2 * static_cast<int>(phases.numel()), interleaved, factor, stream.handle);
       if (rc != ATTN_OK) return status_error(rc, backward ? "attn_rope_bwd" : "attn_rope");
-      if (made) stream.uses(y);
+      if (made) stream.returns(y);
     }
     return THPVariable_Wrap(std::move(y));
   });
@@ -314,17 +326,18 @@ PyObject* paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
       check(B > 0 && T % B == 0, "without q_start, T must be a multiple of the batch");
     }
     const c10::cuda::OptionalCUDAGuard guard(device);
+    const Stream stream(a[16], device.index());
     at::Tensor o, lse, ws;
     const bool made_o = a[13] == Py_None, made_l = a[14] == Py_None;
     if (made_o) {
-      o = new_tensor({T, Hq, d}, at::kBFloat16, device);
+      o = stream.alloc([&] { return new_tensor({T, Hq, d}, at::kBFloat16, device); });
     } else {
       o = must_be_tensor(a[13], "out");
       check(o.sizes() == q.sizes() && o.scalar_type() == at::kBFloat16 && o.is_contiguous() && o.device() == device,
             "out must be a contiguous bf16 tensor shaped like q on q's device");
     }
     if (made_l) {
-      lse = new_tensor({T, Hq}, at::kFloat, device);
+      lse = stream.alloc([&] { return new_tensor({T, Hq}, at::kFloat, device); });
     } else {
       lse = must_be_tensor(a[14], "lse");
       check(lse.dim() == 2 && lse.size(0) == T && lse.size(1) == Hq && lse.scalar_type() == at::kFloat && lse.is_contiguous() &&
@@ -342,26 +355,22 @@ PyObject* paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
                              : integer32(a[12], "num_splits");
       void* ws_ptr = nullptr;
       size_t ws_bytes = 0;
-      bool made_w = false;
       if (a[15] != Py_None) {
         ws = must_be_tensor(a[15], "workspace");
         check(ws.device() == device && ws.is_contiguous(), "workspace must be a contiguous tensor on q's device");
         ws_bytes = ws.nbytes();
       } else if ((ws_bytes = attn_fwd_fp8_paged_workspace_size(T, Hq, c.heads, d, max_q, splits)) > 0) {
-        ws = new_tensor({static_cast<int64_t>(ws_bytes)}, at::kByte, device);
-        made_w = true;
+        ws = stream.alloc([&] { return new_tensor({static_cast<int64_t>(ws_bytes)}, at::kByte, device); });
       }
       if (ws.defined()) ws_ptr = ws.data_ptr();
-      const Stream stream(a[16], device.index());
       const int rc = attn_fwd_fp8_paged(
           q.data_ptr(), q.stride(0), q.stride(1), c.k->data_ptr(), c.v->data_ptr(), static_cast<const float*>(c.ks->data_ptr()),
           static_cast<const float*>(c.vs->data_ptr()), static_cast<const int32_t*>(table.data_ptr()), width, start,
           static_cast<const int32_t*>(lens.data_ptr()), o.data_ptr(), static_cast<float*>(lse.data_ptr()), B, T, Hq, c.heads, d,
           c.pages, c.page_size, max_q, max_kv, scale, causal, splits, ws_ptr, ws_bytes, stream.handle);
       if (rc != ATTN_OK) return status_error(rc, "attn_fwd_fp8_paged");
-      if (made_o) stream.uses(o);
-      if (made_l) stream.uses(lse);
-      if (made_w) stream.uses(ws);
+      if (made_o) stream.returns(o);
+      if (made_l) stream.returns(lse);
     }
     PyObject* po = THPVariable_Wrap(std::move(o));
     PyObject* pl = THPVariable_Wrap(std::move(lse));
