@@ -140,6 +140,12 @@ at::Tensor new_like(const at::Tensor& x) {
   return new_tensor(x.sizes(), x.scalar_type(), x.device());
 }
 
+// Counts a write into a tensor of the caller's, as torch's in-place operations do: autograd then refuses a value
+// that it saved and that has changed since.  (Inference tensors have no count, and autograd saves none.)
+void written(const at::Tensor& t) {
+  if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 int dim32(int64_t n, const char* name) {
   if (n > INT32_MAX) value_error(std::string(name) + " does not fit 32 bits");
   return static_cast<int>(n);
@@ -225,6 +231,7 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
           2 * static_cast<int>(phases.numel()), interleaved, factor, stream.handle);
       if (rc != ATTN_OK) return status_error(rc, backward ? "attn_rope_bwd" : "attn_rope");
       if (made) stream.returns(y);
+      else written(y);
     }
     return THPVariable_Wrap(std::move(y));
   });
@@ -297,6 +304,7 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
                                          factor, c.k->data_ptr(), c.v->data_ptr(), static_cast<float*>(c.ks->data_ptr()),
                                          static_cast<float*>(c.vs->data_ptr()), c.pages, c.page_size, stream.handle);
     if (rc != ATTN_OK) return status_error(rc, "attn_paged_append_fp8");
+    for (const at::Tensor* t : {c.k, c.v, c.ks, c.vs}) written(*t);
     Py_RETURN_NONE;
   });
 }
@@ -370,7 +378,9 @@ PyObject* paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
           c.pages, c.page_size, max_q, max_kv, scale, causal, splits, ws_ptr, ws_bytes, stream.handle);
       if (rc != ATTN_OK) return status_error(rc, "attn_fwd_fp8_paged");
       if (made_o) stream.returns(o);
+      else written(o);
       if (made_l) stream.returns(lse);
+      else written(lse);
     }
     PyObject* po = THPVariable_Wrap(std::move(o));
     PyObject* pl = THPVariable_Wrap(std::move(lse));
