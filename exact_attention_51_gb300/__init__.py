@@ -132,6 +132,9 @@ def load_library(path: str = LIB_PATH):
                                            + [_int] * 9 + [_flt, _int, _int, _vp, ctypes.c_size_t,
                                                            _vp])
         lib.attn_fwd_fp8_paged.restype = _int
+        lib.attn_selftest_fwd_fp8_paged_dropped_load.argtypes = (
+            lib.attn_fwd_fp8_paged.argtypes[:-1] + [_int, ctypes.c_uint, _vp])
+        lib.attn_selftest_fwd_fp8_paged_dropped_load.restype = _int
         lib.attn_fwd_fp8_paged_workspace_size.argtypes = [_int] * 6
         lib.attn_fwd_fp8_paged_workspace_size.restype = ctypes.c_size_t
         lib.attn_fwd_fp8_paged_num_splits.argtypes = [_int] * 8
@@ -519,6 +522,32 @@ def attn_selftest_fwd_dropped_load(q, k, v, out, lse, causal: bool, drop_load: i
             q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H, N, d,
             float(scale), int(bool(causal)), int(drop_load), int(timeout_ms),
             _stream_handle(stream, q.device)))
+
+
+def attn_selftest_fwd_fp8_paged_dropped_load(q, k_cache, v_cache, k_scale, v_scale, block_table,
+                                             kv_len, q_start, max_q: int, max_kv: int,
+                                             num_splits: int, drop_load: int,
+                                             timeout_ms: int = 50, causal: bool = True,
+                                             stream=None) -> int:
+    """Enqueue the abort-path self-test of paged attention (see
+    include/attn_paged.h): ``attn_fwd_fp8_paged`` on these tensors with one load
+    left out and every wait limited to ``timeout_ms``.  Returns the C status; the
+    outcome is read with ``attn_fwd_device_status``."""
+    import torch
+    T, Hq, d = q.shape
+    Hkv, (B, width) = k_cache.shape[1], block_table.shape
+    out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    need = attn_fwd_fp8_paged_workspace_size(T, Hq, Hkv, d, max_q, num_splits)
+    workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+    with torch.cuda.device(q.device):
+        return int(load_library().attn_selftest_fwd_fp8_paged_dropped_load(
+            q.data_ptr(), q.stride(0), q.stride(1), k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), width,
+            q_start.data_ptr(), kv_len.data_ptr(), out.data_ptr(), lse.data_ptr(), B, T, Hq, Hkv,
+            d, k_cache.shape[0], k_cache.shape[2], max_q, max_kv, 1.0 / math.sqrt(d),
+            int(bool(causal)), num_splits, workspace.data_ptr(), need, int(drop_load),
+            int(timeout_ms), _stream_handle(stream, q.device)))
 
 
 def attn_fwd_device_status(stream=None, device=None):

@@ -156,86 +156,15 @@ cudaError_t launch_paged_combine(int d, const PagedParams& p, cudaStream_t strea
                     : chain_launch(paged_combine_kernel<256, 8>, rows, 256, 0, stream, 1, p);
 }
 
-}  // namespace ea51
+namespace {
 
-using namespace ea51;
-
-extern "C" {
-
-size_t attn_fwd_fp8_paged_workspace_size(int T, int Hq, int Hkv, int d, int max_q, int num_splits) {
-  if (T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !head_dim(d) || max_q < 1) return 0;
-  if (num_splits < 1 || num_splits > kMaxKvSplits || static_cast<long long>(T) * Hq > 0x7fffffffLL) return 0;
-  const long long rows = static_cast<long long>(std::min(max_q, T)) * (Hq / Hkv);
-  return paged_bytes(T, Hq, d, num_splits / paged_cluster(paged_rows(d, rows), num_splits), nullptr);
-}
-
-int attn_fwd_fp8_paged_num_splits(int B, int Hq, int Hkv, int d, int page_size, int max_q,
-                                  int max_kv, int num_sms) {
-  if (!page_tokens(page_size)) return 1;
-  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !head_dim(d) || max_q < 1 || max_kv < 1 || num_sms < 1)
-    return 1;
-  const long long rows = static_cast<long long>(max_q) * (Hq / Hkv);
-  const int tile_rows = paged_rows(d, rows);
-  const double ctas = static_cast<double>((rows + tile_rows - 1) / tile_rows) * B * Hkv;
-  // Modelled run time in us, from measured parts (GB300); a turn is kPagedUnit keys of one block.  A batch's lengths are
-  // on the device: what is smallest is the product of its time if all are max_kv and of that if they fill 0.35 of it,
-  // the longest among them.  Over 12 batches (3 to 32 sequences of 2048 to 16384 keys, each head dim), all of one
-  // length and of lengths from an eighth on, the counts taken cost 9 % more than each's best, and 15 % with the full
-  // length alone.
-  const double partial = static_cast<double>(B) * max_q * Hq * d * 8.0 / 5e6;  // a split's output, out and back
-  const bool long_tile = tile_rows >= kPrefillRows;
-  // Rows of the matrix instruction that are not used cost the split-KV kernel little, two tiles of eight a fifth.
-  const double wide = tile_rows == 16 ? 1.2 : 1.0;
-  const double alone = (d == 256 ? 2.2 : 1.1) * wide;  // a turn's latency; 1.4 times that with company
-  const double bytes = 0.73 * d / 128.0 * wide;        // a turn's share of the multiprocessor's bandwidth
-  const double resident = paged_blocks(d, tile_rows, page_size);
-  double best = 0;
-  int best_s = 1;
-  for (int s = 1; s <= kMaxKvSplits; ++s) {
-    const double turns = std::ceil(std::ceil(static_cast<double>(max_kv) / kPagedUnit) / s);
-    const double per_sm = ctas * s / num_sms;
-    double t;
-    if (long_tile) {
-      // A turn of the tcgen05 kernel takes 1.75 us at each head dim, to begin and end a block 10, the merge in a cluster
-      // 6; clusters of 3 and 4 leave multiprocessors empty, and a last wave in halves takes half a wave.  Measured
-      // over nine shapes (64 to 4096
-      // queries of 8192 to 32768 keys), the count taken was the fastest or within 2 % of it.
-      const bool cluster = s > 1 && s <= kPrefillCluster;
-      double queue = per_sm <= 1.0 ? 1.0 : 0.5 * (std::ceil(per_sm) + per_sm) * (cluster && s > 2 ? 1.08 : 1.0);
-      if (s == 1 && paged_tail(static_cast<long long>(ctas), num_sms, max_q, max_kv, true) > 0)
-        queue = std::min(queue, std::floor(per_sm) + 0.5);
-      t = 4.0 + queue * (turns * 1.75 + 10.0 + (cluster ? 6.0 : 0.0)) + (s > kPrefillCluster ? 3.0 + partial * s : 0.0);
-    } else {
-      // Clusters want all their blocks at once (B=64 up to 16384 keys, 32/8 heads: 165 us in clusters of 4 to 8, 133 with
-      // 9 to 12 splits and the merge kernel), and large ones do not fill the groups of multiprocessors that each has to fit
-      // in (288 blocks of 304 in clusters of 6: 54 us, 240 in clusters of 5: 36).
-      t = 1.0;
-      for (const double fill : {1.0, 0.35}) {
-        if (fill < 1.0 && B == 1) continue;
-        const double held = per_sm * fill, waves = held / resident;
-        const bool crowded = s > 1 && s <= kPagedCluster && waves > (s > 4 ? 0.85 : 1.0);
-        const double latency = turns * alone * (held > 1.0 ? 1.4 : 1.0);
-        const double queue = waves > 1.0 ? 1.0 + (std::ceil(waves) / waves - 1.0) * (B > 1 ? 0.3 : 1.0) : 1.0;
-        const double through = held * (turns * bytes + 2.0) * queue;  // (2 us of it to begin and end a block)
-        t *= (s > kPagedCluster ? 11.0 + partial * s : 4.0) +
-             (std::max(latency, through) + 0.1 * std::min(latency, through)) * (crowded ? 1.4 : 1.0);
-      }
-    }
-    if (s == 1 || t < best) {
-      best = t;
-      best_s = s;
-    }
-  }
-  return best_s;
-}
-
-int attn_fwd_fp8_paged(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_cache,
-                       const void* v_cache, const float* k_scale, const float* v_scale,
-                       const int32_t* block_table, int table_stride, const int32_t* q_start,
-                       const int32_t* kv_len, void* o, float* lse, int B, int T, int Hq, int Hkv,
-                       int d, int num_pages, int page_size, int max_q, int max_kv, float scale,
-                       int causal, int num_splits, void* workspace, size_t workspace_bytes,
-                       void* stream) {
+int paged_forward(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_cache,
+                  const void* v_cache, const float* k_scale, const float* v_scale,
+                  const int32_t* block_table, int table_stride, const int32_t* q_start,
+                  const int32_t* kv_len, void* o, float* lse, int B, int T, int Hq, int Hkv,
+                  int d, int num_pages, int page_size, int max_q, int max_kv, float scale,
+                  int causal, int num_splits, void* workspace, size_t workspace_bytes,
+                  int drop_load, unsigned long long wait_timeout_ns, void* stream) {
   if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !kv_len || !o || !lse)
     return ATTN_ERR_INVALID_ARG;
   if (B < 1 || T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !head_dim(d)) return ATTN_ERR_INVALID_ARG;
@@ -329,11 +258,111 @@ int attn_fwd_fp8_paged(const void* q, int64_t q_stride_t, int64_t q_stride_h, co
   const long long units = (static_cast<long long>(max_kv) + kPagedUnit - 1) / kPagedUnit;
   p.chunk = static_cast<int>(std::min<long long>((units + num_splits - 1) / num_splits * kPagedUnit, 1LL << 30));
   p.causal = causal != 0;
+  p.wait_timeout_ns = wait_timeout_ns, p.drop_load = drop_load;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = launch_paged(d, tile_rows, &tk, &tv, p, st);
   if (e == cudaSuccess && p.shares > 1) e = launch_paged_combine(d, p, st);
   return e == cudaSuccess ? ATTN_OK : record_cuda_error(e);
+}
+
+}  // namespace
+}  // namespace ea51
+
+using namespace ea51;
+
+extern "C" {
+
+size_t attn_fwd_fp8_paged_workspace_size(int T, int Hq, int Hkv, int d, int max_q, int num_splits) {
+  if (T < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !head_dim(d) || max_q < 1) return 0;
+  if (num_splits < 1 || num_splits > kMaxKvSplits || static_cast<long long>(T) * Hq > 0x7fffffffLL) return 0;
+  const long long rows = static_cast<long long>(std::min(max_q, T)) * (Hq / Hkv);
+  return paged_bytes(T, Hq, d, num_splits / paged_cluster(paged_rows(d, rows), num_splits), nullptr);
+}
+
+int attn_fwd_fp8_paged_num_splits(int B, int Hq, int Hkv, int d, int page_size, int max_q,
+                                  int max_kv, int num_sms) {
+  if (!page_tokens(page_size)) return 1;
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || !head_dim(d) || max_q < 1 || max_kv < 1 || num_sms < 1)
+    return 1;
+  const long long rows = static_cast<long long>(max_q) * (Hq / Hkv);
+  const int tile_rows = paged_rows(d, rows);
+  const double ctas = static_cast<double>((rows + tile_rows - 1) / tile_rows) * B * Hkv;
+  // Modelled run time in us, from measured parts (GB300); a turn is kPagedUnit keys of one block.  A batch's lengths are
+  // on the device: what is smallest is the product of its time if all are max_kv and of that if they fill 0.35 of it,
+  // the longest among them.  Over 12 batches (3 to 32 sequences of 2048 to 16384 keys, each head dim), all of one
+  // length and of lengths from an eighth on, the counts taken cost 9 % more than each's best, and 15 % with the full
+  // length alone.
+  const double partial = static_cast<double>(B) * max_q * Hq * d * 8.0 / 5e6;  // a split's output, out and back
+  const bool long_tile = tile_rows >= kPrefillRows;
+  // Rows of the matrix instruction that are not used cost the split-KV kernel little, two tiles of eight a fifth.
+  const double wide = tile_rows == 16 ? 1.2 : 1.0;
+  const double alone = (d == 256 ? 2.2 : 1.1) * wide;  // a turn's latency; 1.4 times that with company
+  const double bytes = 0.73 * d / 128.0 * wide;        // a turn's share of the multiprocessor's bandwidth
+  const double resident = paged_blocks(d, tile_rows, page_size);
+  double best = 0;
+  int best_s = 1;
+  for (int s = 1; s <= kMaxKvSplits; ++s) {
+    const double turns = std::ceil(std::ceil(static_cast<double>(max_kv) / kPagedUnit) / s);
+    const double per_sm = ctas * s / num_sms;
+    double t;
+    if (long_tile) {
+      // A turn of the tcgen05 kernel takes 1.75 us at each head dim, to begin and end a block 10, the merge in a cluster
+      // 6; clusters of 3 and 4 leave multiprocessors empty, and a last wave in halves takes half a wave.  Measured
+      // over nine shapes (64 to 4096
+      // queries of 8192 to 32768 keys), the count taken was the fastest or within 2 % of it.
+      const bool cluster = s > 1 && s <= kPrefillCluster;
+      double queue = per_sm <= 1.0 ? 1.0 : 0.5 * (std::ceil(per_sm) + per_sm) * (cluster && s > 2 ? 1.08 : 1.0);
+      if (s == 1 && paged_tail(static_cast<long long>(ctas), num_sms, max_q, max_kv, true) > 0)
+        queue = std::min(queue, std::floor(per_sm) + 0.5);
+      t = 4.0 + queue * (turns * 1.75 + 10.0 + (cluster ? 6.0 : 0.0)) + (s > kPrefillCluster ? 3.0 + partial * s : 0.0);
+    } else {
+      // Clusters want all their blocks at once (B=64 up to 16384 keys, 32/8 heads: 165 us in clusters of 4 to 8, 133 with
+      // 9 to 12 splits and the merge kernel), and large ones do not fill the groups of multiprocessors that each has to fit
+      // in (288 blocks of 304 in clusters of 6: 54 us, 240 in clusters of 5: 36).
+      t = 1.0;
+      for (const double fill : {1.0, 0.35}) {
+        if (fill < 1.0 && B == 1) continue;
+        const double held = per_sm * fill, waves = held / resident;
+        const bool crowded = s > 1 && s <= kPagedCluster && waves > (s > 4 ? 0.85 : 1.0);
+        const double latency = turns * alone * (held > 1.0 ? 1.4 : 1.0);
+        const double queue = waves > 1.0 ? 1.0 + (std::ceil(waves) / waves - 1.0) * (B > 1 ? 0.3 : 1.0) : 1.0;
+        const double through = held * (turns * bytes + 2.0) * queue;  // (2 us of it to begin and end a block)
+        t *= (s > kPagedCluster ? 11.0 + partial * s : 4.0) +
+             (std::max(latency, through) + 0.1 * std::min(latency, through)) * (crowded ? 1.4 : 1.0);
+      }
+    }
+    if (s == 1 || t < best) {
+      best = t;
+      best_s = s;
+    }
+  }
+  return best_s;
+}
+
+int attn_fwd_fp8_paged(const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_cache,
+                       const void* v_cache, const float* k_scale, const float* v_scale,
+                       const int32_t* block_table, int table_stride, const int32_t* q_start,
+                       const int32_t* kv_len, void* o, float* lse, int B, int T, int Hq, int Hkv,
+                       int d, int num_pages, int page_size, int max_q, int max_kv, float scale,
+                       int causal, int num_splits, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  return paged_forward(q, q_stride_t, q_stride_h, k_cache, v_cache, k_scale, v_scale, block_table, table_stride, q_start,
+                       kv_len, o, lse, B, T, Hq, Hkv, d, num_pages, page_size, max_q, max_kv, scale, causal, num_splits,
+                       workspace, workspace_bytes, -1, kWaitTimeoutNs, stream);
+}
+
+int attn_selftest_fwd_fp8_paged_dropped_load(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_cache, const void* v_cache, const float* k_scale,
+    const float* v_scale, const int32_t* block_table, int table_stride, const int32_t* q_start, const int32_t* kv_len,
+    void* o, float* lse, int B, int T, int Hq, int Hkv, int d, int num_pages, int page_size, int max_q, int max_kv,
+    float scale, int causal, int num_splits, void* workspace, size_t workspace_bytes, int drop_load,
+    unsigned int timeout_ms, void* stream) {
+  if (drop_load < 0 || timeout_ms < 1 || timeout_ms > 10000) return ATTN_ERR_INVALID_ARG;
+  return paged_forward(q, q_stride_t, q_stride_h, k_cache, v_cache, k_scale, v_scale, block_table, table_stride, q_start,
+                       kv_len, o, lse, B, T, Hq, Hkv, d, num_pages, page_size, max_q, max_kv, scale, causal, num_splits,
+                       workspace, workspace_bytes, drop_load, static_cast<unsigned long long>(timeout_ms) * 1000000ull,
+                       stream);
 }
 
 }  // extern "C"

@@ -34,6 +34,8 @@ struct PagedParams {
   int tail_tile;      // tcgen05 kernel: row tiles from here on, the last wave's, are a cluster's of two; 0: none
   int causal;
   float scale_log2;  // scale * log2(e)
+  unsigned long long wait_timeout_ns;  // limit of each bounded wait
+  int drop_load;  // a test hook: this load is left out (-1: none); see attn_selftest_fwd_fp8_paged_dropped_load
 };
 
 constexpr unsigned kCodeBadPage = 0x202, kCodeBadSequence = 0x203;

@@ -98,10 +98,7 @@ struct PrefillShape {
   // a cluster's merge: each row's output, maximum and sum, where the tiles were (rows padded by 16 bytes: the
   // threads of a warp write a row each)
   static constexpr int R = ROWS, MERGE_THREADS = NQ * 128, PART_PITCH = D + 4;
-  // Blocks whose parts it reads at once; more than kPrefillCluster are not there.  It is written so for the softmax's
-  // loop, whose registers the compiler shares out with the merge in view: 2 x 2048 queries against 16384 keys, all in
-  // one launch, with 4 and 8: d = 64 358 us and 379, d = 128 905 and 822, d = 256 (1024 queries) 482 and 450.
-  static constexpr int MERGE_BLOCKS = D == 64 ? kPrefillCluster : kPagedCluster;
+  static constexpr int MERGE_BLOCKS = kPrefillCluster;  // blocks whose parts it reads at once
   static constexpr int OFF_PART = 0, OFF_BLOCK = R * PART_PITCH * 4;
   static_assert(OFF_BLOCK + 2 * R * 4 <= OFF_META, "the merge's rows");
   __host__ __device__ static constexpr int s_col(int q, int b) { return (q * NSB + b) * BN; }
@@ -220,7 +217,7 @@ __device__ void prefill_load(const CUtensorMap* tm_k, const CUtensorMap* tm_v, c
   int pg_next = page_at(1);
   const bool starts_box = lane < S::GROUPS && (16 * lane) % box_rows == 0;
   begin();
-  int issued[2] = {0, 0};  // tiles of K and of V whose copies may be in flight
+  int issued[2] = {0, 0};  // tiles of K and of V
   bool ok = true;
   for (int j = 0; j < t.n && ok; ++j) {
     const bool mine = starts_box && pg >= 0;
@@ -247,6 +244,8 @@ __device__ void prefill_load(const CUtensorMap* tm_k, const CUtensorMap* tm_v, c
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(S::B_META + j % kMetaDepth));
       }
+      issued[kv] = j + 1;
+      if (2 * j + kv == p.drop_load) continue;  // test hook: this slot never fills
       if (lane == 0) mbar_arrive_expect_tx(bar(kFull[kv] + st), boxes * S::PANELS8 * box);
       __syncwarp();
       if (mine) {
@@ -256,19 +255,19 @@ __device__ void prefill_load(const CUtensorMap* tm_k, const CUtensorMap* tm_v, c
         for (int pn = 0; pn < S::PANELS8; ++pn)
           tma_load_3d(dst + pn * S::RAW_PANEL, kv ? tm_v : tm_k, bar(kFull[kv] + st), pn * S::PW, row, pg * p.Hkv + t.h);
       }
-      issued[kv] = j + 1;
     }
     if (!ok) break;
     pg = pg_next;
     scales(pg);
     pg_next = page_at(j + 2);
   }
-  if (*w.abort_flag) {
-    for (int i = max(0, issued[0] - S::KS); i < issued[0]; ++i)
+  // no copy is in flight when the block ends, whoever's wait gives up before the tile is used
+  for (int i = max(0, issued[0] - S::KS); i < issued[0]; ++i)
+    if (2 * i != p.drop_load)
       drain_phase(bar(S::B_KFULL + i % S::KS), static_cast<uint32_t>(i / S::KS) & 1u, w, kCodeDrain);
-    for (int i = max(0, issued[1] - S::VS); i < issued[1]; ++i)
+  for (int i = max(0, issued[1] - S::VS); i < issued[1]; ++i)
+    if (2 * i + 1 != p.drop_load)
       drain_phase(bar(S::B_VFULL + i % S::VS), static_cast<uint32_t>(i / S::VS) & 1u, w, kCodeDrain);
-  }
 }
 
 // Bytes of a word that are NaN codes, as 0xff each.
@@ -901,7 +900,10 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   if (!prefill_tile<S>(p, t, threadIdx.x == 0)) return;
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + S::OFF_ABORT);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::OFF_TMEMSLOT);
-  const Waiter w{abort_flag, p.status};
+  // The warps that wait for copies have the caller's limit.  The softmax, which the abort flag stops, has the usual one as a
+  // constant: its loop takes up to 7 % longer or shorter by what else the compiler keeps in its registers (2 x 2048
+  // queries against 16384 keys, d = 128: 837 us so, 890 with the limit from the parameters).
+  const Waiter w{abort_flag, p.status, p.wait_timeout_ns}, w_softmax{abort_flag, p.status};
   // for the epilogue, so that the softmax does not keep it in registers where those are short
   static_assert(sizeof(PrefillTile<S>) <= 96, "the tile's place");
   const PrefillTile<S>& tile = S::SPLIT_REGS ? *reinterpret_cast<const PrefillTile<S>*>(smem + S::OFF_TILE) : t;
@@ -935,7 +937,7 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     const uint32_t tmem = begin();
     if constexpr (S::SPLIT_REGS) setmaxnreg_inc<S::REG_SOFTMAX>();
     if constexpr (S::D == 128) prefill_fetch<S>(q, p, t, rows);
-    const PrefillRow<S> row = prefill_softmax<S>(q, tmem, smem, sbase, tile, p, rows, w);
+    const PrefillRow<S> row = prefill_softmax<S>(q, tmem, smem, sbase, tile, p, rows, w_softmax);
     tc_fence_after_sync();
     if (tile.cluster == 1 && (row.has || tile.nkv[q] == 0))  // (not if a wait gave up)
       prefill_store<S>(q, tmem, sbase, tile, p, row);

@@ -135,6 +135,24 @@ ATTN_API size_t attn_fwd_fp8_paged_workspace_size(int T, int Hq, int Hkv, int d,
 ATTN_API int attn_fwd_fp8_paged_num_splits(int B, int Hq, int Hkv, int d, int page_size, int max_q,
                                            int max_kv, int num_sms);
 
+/*
+ * Self-test of the kernels' own abort path (a test hook, not a way to compute
+ * attention), as attn_selftest_fwd_dropped_load: attn_fwd_fp8_paged on the given
+ * arguments, except that every thread block leaves out one load and every wait gives
+ * up after `timeout_ms` (1..10000) milliseconds.  drop_load >= 0: up to 16 rows, the ring's stage of
+ * that number (128 keys each, 64 at d = 256 in pages of 16); more rows, 2 j for the keys and 2 j + 1 for the values of the
+ * block's key tile j (128 keys, 64 at d = 256).  Blocks with fewer run to the end.  O and LSE are
+ * not valid afterwards; attn_fwd_device_status returns ATTN_ERR_TIMEOUT with the code of the
+ * wait that gave up first (0x14x up to 16 rows, 0x15x more) and clears the word.  Run it only when
+ * no other launch of the library is in flight on the device.
+ */
+ATTN_API int attn_selftest_fwd_fp8_paged_dropped_load(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_cache, const void* v_cache,
+    const float* k_scale, const float* v_scale, const int32_t* block_table, int table_stride,
+    const int32_t* q_start, const int32_t* kv_len, void* o, float* lse, int B, int T, int Hq, int Hkv,
+    int d, int num_pages, int page_size, int max_q, int max_kv, float scale, int causal, int num_splits,
+    void* workspace, size_t workspace_bytes, int drop_load, unsigned int timeout_ms, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

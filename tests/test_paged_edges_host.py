@@ -1,5 +1,15 @@
-"""Arithmetic that paged attention relies on, without a GPU."""
+"""Arithmetic that paged attention relies on and refusals of its entry points, without a
+GPU (every call here is refused or does no device work)."""
+import pytest
 import torch
+
+import exact_attention_51_gb300 as ea
+from exact_attention_51_gb300 import build as eabuild
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    eabuild.build()
 
 
 def test_every_bf16_value_in_two_8_bit_parts():
@@ -11,3 +21,16 @@ def test_every_bf16_value_in_two_8_bit_parts():
     rest = x - first
     off = (rest - rest.to(torch.float8_e5m2).float()).abs()
     assert off[x >= 2.0 ** -6].max() == 0 and off.max() <= 2.0 ** -14
+
+
+A = 1 << 20  # fake, aligned "device" addresses (never dereferenced)
+
+
+@pytest.mark.parametrize("kw", [dict(drop=-1), dict(ms=0), dict(ms=10001), dict(T=0), dict(splits=65), dict(d=96)])
+def test_paged_selftest_refuses(kw):
+    a = dict(T=6, d=64, splits=1, drop=0, ms=50) | kw
+    lib = ea.load_library()
+    assert lib.attn_selftest_fwd_fp8_paged_dropped_load(
+        A, 8 * 64, 64, A + (1 << 34), A + (1 << 35), A + (1 << 36), A + (1 << 37), A + (1 << 30), 7, A + (1 << 31), A + (1 << 32),
+        A + (1 << 38), A + (1 << 39), 3, a["T"], 8, 2, a["d"], 9, 16, 2, 100, 0.125, 1, a["splits"], None, 0, a["drop"], a["ms"],
+        None) == ea.ATTN_ERR_INVALID_ARG
