@@ -272,6 +272,7 @@ int rope(const void* x, void* y, int dtype, int B, int H, int N, int d, long lon
   for (const auto& [stride, count] :
        {std::pair<long long, long long>{xs_b, B}, {xs_h, H}, {xs_n, N}, {ys_b, B}, {ys_h, H}, {ys_n, N}})
     if (stride < 0 || (count > 1 && stride > kMost / count)) return ATTN_ERR_INVALID_ARG;
+  if (pos && B > 1 && pos_stride_b > kMost / B) return ATTN_ERR_INVALID_ARG;
   if (!distinct(B, H, N, d, ys_b, ys_h, ys_n)) return ATTN_ERR_INVALID_ARG;
   const size_t es = dtype == ATTN_ROPE_F32 ? 4 : 2;
   const uintptr_t xa = reinterpret_cast<uintptr_t>(x), ya = reinterpret_cast<uintptr_t>(y);

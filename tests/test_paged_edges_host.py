@@ -34,3 +34,13 @@ def test_paged_selftest_refuses(kw):
         A, 8 * 64, 64, A + (1 << 34), A + (1 << 35), A + (1 << 36), A + (1 << 37), A + (1 << 30), 7, A + (1 << 31), A + (1 << 32),
         A + (1 << 38), A + (1 << 39), 3, a["T"], 8, 2, a["d"], 9, 16, 2, 100, 0.125, 1, a["splits"], None, 0, a["drop"], a["ms"],
         None) == ea.ATTN_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("entry", ["attn_rope", "attn_rope_bwd"])
+@pytest.mark.parametrize("stride", [1 << 62, 1 << 46, (1 << 61) + 5])
+def test_rope_refuses_position_strides_that_wrap(entry, stride):
+    """As of x and y: (B - 1) strides of 2^62 wrap to 0 for B = 5, an extent that overlaps nothing."""
+    st = (3 * 5 * 64, 5 * 64, 64)
+    rc = getattr(ea.load_library(), entry)(A, A + (1 << 30), 0, 5, 3, 5, 64, *st, *st, A + (1 << 34), stride, 0, A + (1 << 35), 64,
+                                           0, 1.0, None)
+    assert rc == ea.ATTN_ERR_INVALID_ARG
