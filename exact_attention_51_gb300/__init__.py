@@ -589,6 +589,11 @@ def _load_binding():
     return _fast
 
 
+def _fits(*values) -> bool:
+    """Whether these are 32-bit integers: ctypes cuts larger ones off."""
+    return all(-(1 << 31) <= v < 1 << 31 for v in values)
+
+
 def attn_rope_phases(rot_dim: int, base: float = 10000.0, scaling: str = "none",
                      factor: float = 1.0, original_positions: int = 4096, beta_fast: float = 32.0,
                      beta_slow: float = 1.0, device=None):
@@ -606,7 +611,9 @@ def attn_rope_phases(rot_dim: int, base: float = 10000.0, scaling: str = "none",
     import torch
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALINGS)}")
-    phases = torch.empty(max(int(rot_dim) // 2, 1), dtype=torch.int64)
+    if not 2 <= rot_dim <= 512 or not _fits(original_positions):  # (before they are cut to 32 bits)
+        raise AttnError(ATTN_ERR_INVALID_ARG, "attn_rope_phases")
+    phases = torch.empty(int(rot_dim) // 2, dtype=torch.int64)
     attention = _flt(0.0)
     rc = load_library().attn_rope_phases(phases.data_ptr(), ctypes.byref(attention), int(rot_dim),
                                          float(base), ROPE_SCALINGS[scaling], float(factor),
@@ -669,11 +676,15 @@ def attn_paged_append_fp8(k, v, slots, k_cache, v_cache, k_scale, v_scale, phase
 
 def attn_fwd_fp8_paged_workspace_size(T: int, Hq: int, Hkv: int, d: int, max_q: int,
                                       num_splits: int) -> int:
+    if not _fits(T, Hq, Hkv, d, max_q, num_splits):
+        return 0
     return int(load_library().attn_fwd_fp8_paged_workspace_size(T, Hq, Hkv, d, max_q, num_splits))
 
 
 def attn_fwd_fp8_paged_num_splits(B: int, Hq: int, Hkv: int, d: int, page_size: int, max_q: int,
                                   max_kv: int, num_sms: int) -> int:
+    if not _fits(B, Hq, Hkv, d, page_size, max_q, max_kv, num_sms):
+        return 1
     return int(load_library().attn_fwd_fp8_paged_num_splits(B, Hq, Hkv, d, page_size, max_q,
                                                             max_kv, num_sms))
 

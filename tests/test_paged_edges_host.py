@@ -44,3 +44,26 @@ def test_rope_refuses_position_strides_that_wrap(entry, stride):
     rc = getattr(ea.load_library(), entry)(A, A + (1 << 30), 0, 5, 3, 5, 64, *st, *st, A + (1 << 34), stride, 0, A + (1 << 35), 64,
                                            0, 1.0, None)
     assert rc == ea.ATTN_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(rot_dim=(1 << 32) + 64), dict(rot_dim=-(1 << 32) + 64), dict(rot_dim=1 << 40), dict(rot_dim=-64),
+                                dict(scaling="yarn", factor=2.0, original_positions=(1 << 32) + 4096)])
+def test_phases_refuse_what_does_not_fit(kw):
+    """Not taken for what is left of them in 32 bits, nor allocated first."""
+    with pytest.raises(ea.AttnError):
+        ea.attn_rope_phases(**({"rot_dim": 64, "device": "cpu"} | kw))
+
+
+def test_paged_sizes_of_what_does_not_fit():
+    big = 1 << 32
+    assert ea.attn_fwd_fp8_paged_workspace_size(6, 8, 2, 64, 4, 11) > 0
+    for i, n in enumerate((6, 8, 2, 64, 4, 11)):
+        a = [6, 8, 2, 64, 4, 11]
+        a[i] = n + big
+        assert ea.attn_fwd_fp8_paged_workspace_size(*a) == 0
+    sizes = [1, 32, 8, 128, 16, 1, 131072, 152]
+    assert ea.attn_fwd_fp8_paged_num_splits(*sizes) > 1
+    for i, n in enumerate(sizes):
+        a = list(sizes)
+        a[i] = n + big
+        assert ea.attn_fwd_fp8_paged_num_splits(*a) == 1
