@@ -15,9 +15,10 @@
  * Frequencies are passed as phases: u_i = f_i / (2 pi) * 2^64 mod 2^64, the
  * fraction of a turn that a position adds, in units of 2^-64.  p * u_i mod
  * 2^64 is then the exact angle mod one turn: the reduction of the angle of a
- * far position is one integer product, and positions of any int32 value,
- * negative ones among them, are as accurate as position 0 (the fraction's own
- * error of 2^-65 of a turn grows to 2^-34 at position 2^31).  The angle is cut to
+ * far position is one integer product, at any int32 position, negative ones
+ * among them.  What is left is the fraction's own error times the position: of
+ * attn_rope_phases, which computes in fp64, 2^-52 of a turn (2^-35 at position
+ * 2^17, 2^-21 at 2^31); of a table rounded to the unit 2^-65.  The angle is cut to
  * 2^-32 of a turn, cos and sin and the rotation are fp32 (the two within 2^-22), and the
  * result is rounded once to the tensor's type.
  *
@@ -51,7 +52,8 @@ enum attn_rope_scaling {
 
 /*
  * Fills phases[0 .. rot_dim/2) (host memory) for these frequencies, and
- * *attention_factor (may be NULL) with the scaling's factor on cos and sin.
+ * *attention_factor (may be NULL) with the scaling's factor on cos and sin; in
+ * fp64, each to 2^-52 of a turn.
  *
  *   rot_dim   even, 2..512.          base     finite, > 1.
  *   factor    s: finite, >= 1 (ignored by ATTN_ROPE_NONE).

@@ -1,5 +1,7 @@
 """Arithmetic that paged attention relies on and refusals of its entry points, without a
 GPU (every call here is refused or does no device work)."""
+from decimal import Decimal, getcontext
+
 import pytest
 import torch
 
@@ -67,3 +69,24 @@ def test_paged_sizes_of_what_does_not_fit():
         a = list(sizes)
         a[i] = n + big
         assert ea.attn_fwd_fp8_paged_num_splits(*a) == 1
+
+
+PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+@pytest.mark.parametrize("rot,base", [(2, 10000.0), (64, 10000.0), (128, 1e6), (512, 1.5), (96, 500000.0)])
+@pytest.mark.parametrize("scaling,factor", [("none", 1.0), ("linear", 8.0), ("ntk", 4.0)])
+def test_phases_within_a_fraction_of_a_turn(rot, base, scaling, factor):
+    """f / 2 pi to 2^-52 of a turn.  fp64 rounds by 2^-53: pow's result twice, the exponent, which f e ln(base) of
+    passes on (at most 1 / e of a turn's 2 pi-th), 2 pi, the division and the scaling, NTK's base with three of its own:
+    some 2^-50.4 of f / 2 pi, which is 0.16 at most: 2^-53."""
+    if scaling == "ntk" and rot == 2:
+        return
+    getcontext().prec = 60
+    got, _ = ea.attn_rope_phases(rot, base=base, scaling=scaling, factor=factor, device="cpu")
+    b = Decimal(base)
+    if scaling == "ntk":
+        b *= (Decimal(factor).ln() * rot / (rot - 2)).exp()
+    for i, u in enumerate(got.tolist()):
+        f = (b.ln() * Decimal(-2 * i) / rot).exp() / (Decimal(factor) if scaling == "linear" else 1)
+        assert abs(Decimal(u) / 2 ** 64 - f / (2 * PI)) <= Decimal(2) ** -52
