@@ -82,7 +82,7 @@ def test_phases_within_a_fraction_of_a_turn(rot, base, scaling, factor):
     some 2^-50.4 of f / 2 pi, which is 0.16 at most: 2^-53."""
     if scaling == "ntk" and rot == 2:
         return
-    getcontext().prec = 60
+    getcontext().prec = 40
     got, _ = ea.attn_rope_phases(rot, base=base, scaling=scaling, factor=factor, device="cpu")
     b = Decimal(base)
     if scaling == "ntk":
