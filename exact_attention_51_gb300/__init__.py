@@ -701,8 +701,9 @@ def attn_fwd_fp8_paged(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_le
     ``block_table`` int32 [B, pages], the pages of each sequence in order;
     ``kv_len`` int32 [B], its keys (its queries' own among them);
     ``q_start`` int32 [B + 1], where each sequence's query tokens begin (None: T / B each);
-    ``max_q``, the most query tokens of a sequence (None: T); ``max_kv``, about the longest
-    kv_len (None: what the table holds; only the sharing out of the keys goes by
+    ``max_q``, the most query tokens of a sequence (None: T, which for a batch of
+    several sequences is far too many and costs time: give it, 1 when decoding);
+    ``max_kv``, about the longest kv_len (None: what the table holds; only the sharing out of the keys goes by
     it).  Causal puts the queries at the sequence's last positions.  Returns
     ``(o bf16 [T, Hq, d], lse fp32 [T, Hq])``; a query that sees no key gets 0 and
     -inf, and rows of tokens that no sequence has are left as they were.

@@ -288,14 +288,16 @@ int attn_fwd_fp8_paged_num_splits(int B, int Hq, int Hkv, int d, int page_size, 
   const long long rows = static_cast<long long>(max_q) * (Hq / Hkv);
   const int tile_rows = paged_rows(d, rows);
   const double ctas = static_cast<double>((rows + tile_rows - 1) / tile_rows) * B * Hkv;
-  // Modelled run time in us, from measured parts (GB300); a turn is kPagedUnit keys of one block.  A batch's lengths are
-  // on the device: what is smallest is the product of its time if all are max_kv and of that if they fill 0.35 of it,
-  // the longest among them.  Over 12 batches (3 to 32 sequences of 2048 to 16384 keys, each head dim), all of one
-  // length and of lengths from an eighth on, the counts taken cost 9 % more than each's best, and 15 % with the full
-  // length alone.
+  // Modelled run time in us, from measured parts (GB300); a turn is kPagedUnit keys of one block.
+  // A batch's lengths are on the device: what is smallest is the product of its time if all are
+  // max_kv and of that if they fill 0.35 of it, the longest among them.  Over 12 batches (3 to 32
+  // sequences of 2048 to 16384 keys, each head dim), all of one length and of lengths from an
+  // eighth on, the counts taken cost 9 % more than each's best, and 15 % with the full length
+  // alone.
   const double partial = static_cast<double>(B) * max_q * Hq * d * 8.0 / 5e6;  // a split's output, out and back
   const bool long_tile = tile_rows >= kPrefillRows;
-  // Rows of the matrix instruction that are not used cost the split-KV kernel little, two tiles of eight a fifth.
+  // Rows of the matrix instruction that are not used cost the split-KV kernel little, two tiles of
+  // eight a fifth.
   const double wide = tile_rows == 16 ? 1.2 : 1.0;
   const double alone = (d == 256 ? 2.2 : 1.1) * wide;  // a turn's latency; 1.4 times that with company
   const double bytes = 0.73 * d / 128.0 * wide;        // a turn's share of the multiprocessor's bandwidth
@@ -307,19 +309,20 @@ int attn_fwd_fp8_paged_num_splits(int B, int Hq, int Hkv, int d, int page_size, 
     const double per_sm = ctas * s / num_sms;
     double t;
     if (long_tile) {
-      // A turn of the tcgen05 kernel takes 1.75 us at each head dim, to begin and end a block 10, the merge in a cluster
-      // 6; clusters of 3 and 4 leave multiprocessors empty, and a last wave in halves takes half a wave.  Measured
-      // over nine shapes (64 to 4096
-      // queries of 8192 to 32768 keys), the count taken was the fastest or within 2 % of it.
+      // A turn of the tcgen05 kernel takes 1.75 us at each head dim, to begin and end a block 10,
+      // the merge in a cluster 6; clusters of 3 and 4 leave multiprocessors empty, and a last wave
+      // in halves takes half a wave.  Measured over nine shapes (64 to 4096 queries of 8192 to
+      // 32768 keys), the count taken was the fastest or within 2 % of it.
       const bool cluster = s > 1 && s <= kPrefillCluster;
       double queue = per_sm <= 1.0 ? 1.0 : 0.5 * (std::ceil(per_sm) + per_sm) * (cluster && s > 2 ? 1.08 : 1.0);
       if (s == 1 && paged_tail(static_cast<long long>(ctas), num_sms, max_q, max_kv, true) > 0)
         queue = std::min(queue, std::floor(per_sm) + 0.5);
       t = 4.0 + queue * (turns * 1.75 + 10.0 + (cluster ? 6.0 : 0.0)) + (s > kPrefillCluster ? 3.0 + partial * s : 0.0);
     } else {
-      // Clusters want all their blocks at once (B=64 up to 16384 keys, 32/8 heads: 165 us in clusters of 4 to 8, 133 with
-      // 9 to 12 splits and the merge kernel), and large ones do not fill the groups of multiprocessors that each has to fit
-      // in (288 blocks of 304 in clusters of 6: 54 us, 240 in clusters of 5: 36).
+      // Clusters want all their blocks at once (B=64 up to 16384 keys, 32/8 heads: 165 us in
+      // clusters of 4 to 8, 133 with 9 to 12 splits and the merge kernel), and large ones do not
+      // fill the groups of multiprocessors that each has to fit in (288 blocks of 304 in clusters
+      // of 6: 54 us, 240 in clusters of 5: 36).
       t = 1.0;
       for (const double fill : {1.0, 0.35}) {
         if (fill < 1.0 && B == 1) continue;

@@ -1,11 +1,11 @@
 // Appending keys and values to the paged e4m3 cache: attn_paged_append_fp8 of
 // include/attn_paged.h and its kernel.
 //
-// One thread block takes one run -- the new tokens of one page -- of one head
-// of K or V: it holds the run's (rotated) values in registers, reduces their
+// A run is the new tokens of one page.  A thread block takes one head of K or V and up to a
+// page's worth of tokens (one, where the call has few), and the runs that begin among
+// them in turn: it holds a run's (rotated) values in registers, reduces their
 // largest magnitude, settles the block's scale 2^e and writes the codes; where
-// the scale grows, it rewrites the codes of the tokens before the run.  Blocks
-// whose token does not begin a run end at once.
+// the scale grows, it rewrites the codes of the tokens before the run.
 //
 // Why powers of two: moving a code from scale s to s * 2^j only changes its
 // exponent, so a block whose scale grows token by token holds the same codes
@@ -60,7 +60,7 @@ __device__ __forceinline__ float exp2_int(int e) {  // 2^e, a normal number
   return __uint_as_float(static_cast<unsigned>(e + 127) << 23);
 }
 
-// Sixteen e4m3 codes times `ratio`, rounded to the nearest code.
+// Four e4m3 codes times `ratio`, rounded to the nearest code.
 __device__ __forceinline__ uint32_t rescale_codes(uint32_t codes, float ratio) {
   float f[4];
   asm("{\n\t.reg .b16 lo, hi, a, b, c, d;\n\t.reg .b32 x, y;\n\t"
@@ -164,7 +164,8 @@ __global__ void __launch_bounds__(AppendShape<D, PAGE>::BLOCK, ANY ? 1 : AppendS
   const long long limit = static_cast<long long>(p.num_pages) * PAGE;
 
   // The rows' way from HBM starts before the runs are known: a prompt's tokens are mostly one run.
-  // (A block's own chain -- slots, rows, largest value, codes -- is what bounds this kernel: 3 us of the prompt above.)
+  // (A block's own chain -- slots, rows, largest value, codes -- is what bounds this kernel: 3 us
+  // of the prompt above.)
 #pragma unroll
   for (int i = 0; i < UNITS; ++i) {
     const int r = (tid + i * BLOCK) / UPR, u = (tid + i * BLOCK) % UPR;
@@ -299,11 +300,12 @@ __global__ void __launch_bounds__(AppendShape<D, PAGE>::BLOCK, ANY ? 1 : AppendS
 
 template <int D, int PAGE>
 cudaError_t launch_append(AppendParams p, cudaStream_t stream) {
-  // One token a block keeps a decoding step's latency at one run; where that
-  // would be far more blocks than run at once (one without a run still takes its place), a block looks through
-  // several tokens, up to a page's worth, in which a prompt has one or two runs.  Measured with 2^18 threads in the
-  // grid and 2^20: 700 tokens of 8 heads in 16-token pages 4.6 us and 11.9, 69 x 32 tokens of 4 heads of 64 in pages of
-  // 128 6.1 and 8.3, 512 single tokens of 8 heads in 64-token pages 20.3 and 21.6.
+  // One token a block keeps a decoding step's latency at one run; where that would be far more
+  // blocks than run at once (one without a run still takes its place), a block looks through
+  // several tokens, up to a page's worth, in which a prompt has one or two runs.  Measured with
+  // 2^18 threads in the grid and 2^20: 700 tokens of 8 heads in 16-token pages 4.6 us and 11.9, 69
+  // x 32 tokens of 4 heads of 64 in pages of 128 6.1 and 8.3, 512 single tokens of 8 heads in
+  // 64-token pages 20.3 and 21.6.
   constexpr long long kThreads = 1 << 18;
   const long long all = static_cast<long long>(p.T) * p.Hkv * 2 * AppendShape<D, PAGE>::BLOCK;
   p.tokens_per_block = 1;

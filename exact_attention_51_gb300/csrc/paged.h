@@ -50,9 +50,9 @@ constexpr int kPagedCluster = 8;
 // block of two tiles of 128 rows, one at d = 256.
 constexpr int kPrefillRows = 128;
 
-// Thread blocks on a multiprocessor.  Measured at d = 128 with 64-token pages, two and three: one sequence of 131072
-// keys 48 us and 52, 16 queries a block 226 and 294; with 16-token pages, 64 sequences of up to
-// 16384 keys 148 us and 131.
+// Thread blocks on a multiprocessor.  Measured at d = 128 with 64-token pages, two and three: one
+// sequence of 131072 keys 48 us and 52, 16 queries a block 226 and 294; with 16-token pages, 64
+// sequences of up to 16384 keys 148 us and 131.
 constexpr int paged_blocks(int d, int tile_rows, int page_size) {
   return tile_rows >= kPrefillRows ? 1 : page_size == 16 && (d <= 128 || tile_rows <= 8) ? 3 : 2;
 }
@@ -61,12 +61,14 @@ constexpr int paged_blocks(int d, int tile_rows, int page_size) {
 // fill a group of multiprocessors.
 constexpr int kPrefillCluster = 4;
 
-// First of the row tiles of the tcgen05 kernel that are left for a last, partial wave where blocks take whole tiles (0:
-// all tiles alike).  Two blocks of a cluster share such a tile's keys: 2 x 2048 queries against 16384 keys
-// are 512 tiles, three waves of 152 and 56 that two blocks each take (823 us, 911 without; 192 tiles at d = 64 293 and 367).  The launch is one of clusters
-// of two, and those before take two tiles each: 152 multiprocessors hold 76 of them.  (Of four they would leave some
-// empty in every wave.)  Where the tiles' keys differ much, as in a whole prompt, the longest come first and the short
-// ones fill the gaps already (4096 against 4096: 134 us, 145 in this way).
+// First of the row tiles of the tcgen05 kernel that are left for a last, partial wave where blocks
+// take whole tiles (0: all tiles alike).  Two blocks of a cluster share such a tile's keys: 2 x
+// 2048 queries against 16384 keys are 512 tiles, three waves of 152 and 56 that two blocks each
+// take (833 us, 911 without; 192 tiles at d = 64 293 and 367).  The launch is one of clusters of
+// two, and those before take two tiles each: 152 multiprocessors hold 76 of them.  (Of four they
+// would leave some empty in every wave.)  Where the tiles' keys differ much, as in a whole prompt,
+// the longest come first and the short ones fill the gaps already (4096 against 4096, 32/8 heads of
+// 128: 144 us, 149 with pairs).
 inline long long paged_tail(long long tiles, int num_sms, long long max_q, long long max_kv, bool causal) {
   const long long first = tiles / num_sms * num_sms / 2 * 2, rest = tiles - first;
   // (below 2048 keys a share's begin, end and merge cost what it saves)

@@ -8,12 +8,13 @@
 // sum and output of their own, which are merged at the end.
 //
 // Who fills the ring goes by the page size.  Pages of 32 tokens and more: a fifth warp, by TMA, at
-// most eight copies a stage.  A copy's issue takes the warp that does it some 150 cycles of
-// the 1300 that a turn computes, so the others do not: one sequence of 32768 keys in 64-token pages, 8 heads of
-// 128, one block a head, takes 216 us, and 264 with rings that they fill themselves.  Pages of
-// 16 tokens would need 16 copies a stage, more than that warp gets through (64 sequences of up to
-// 16384 keys: 152 us); there each of the four copies its own keys with cp.async, 16 bytes a lane (SELF;
-// 129 us; by TMA the same, but 12.7 us and 11.1 for nine sequences of up to 3001 keys of 64).
+// most eight copies a stage.  A copy's issue takes the warp that does it some 150 cycles of the
+// 1300 that a turn computes, so the others do not: one sequence of 32768 keys in 64-token pages, 8
+// heads of 128, one block a head, takes 216 us, and 264 with rings that they fill themselves.
+// Pages of 16 tokens would need 16 copies a stage, more than that warp gets through (64 sequences
+// of up to 16384 keys: 152 us); there each of the four copies its own keys with cp.async, 16 bytes
+// a lane (SELF; 129 us; by TMA the same, but 12.7 us and 11.1 for nine sequences of up to 3001 keys
+// of 64).
 //
 // Everything is computed transposed, so that the keys are the 16-wide side of
 // the matrix instruction and the few query rows its 8-wide one:
@@ -29,7 +30,13 @@
 //     p' = exp2(s + log2 vs - M),  O = sum p' v8 / l,  l = sum p' / vs,
 // with M the running maximum of s + log2 vs: the largest contribution to O, not
 // the largest weight, is what fp16's range is centred on, and one matrix
-// product accumulates blocks of any scales.
+// product accumulates blocks of any scales.  (p' leaves fp32's normal range 2^-133 below M, and its key l:
+// a weight that matters only where V's scales differ by more than 2^100.)
+//
+// P is rounded to fp16, by up to 2^-11 of each weight, because two parts of P would be twice the
+// products; l sums p' before that.  The results differ from those of a P in fp32 in 5 to 9 of 100
+// bf16 elements, by a step (2^-11 to 2^-10 of O's norm), and are as far from 64 bits as those are:
+// bf16's own rounding, 0.0016 to 0.0017 of the norm.
 //
 // Layout of the products in registers.  K: lane (g, c) = (lane / 4, lane % 4)
 // reads 16 adjacent bytes (16c + 64j of the row), enough for four k-steps; Q's
@@ -232,8 +239,9 @@ __device__ __forceinline__ uint32_t split_nan(uint32_t x, uint32_t& nan) {
   return keep;
 }
 
-// What a block's scores are multiplied by: its K scale (2^-60 at least) times the row's factor, which may be 0.  The
-// smallest normal number on top, which others round away, keeps a masked -inf one however small they are.
+// What a block's scores are multiplied by: its K scale (2^-60 at least) times the row's factor,
+// which may be 0.  The smallest normal number on top, which others round away, keeps a masked -inf
+// one however small they are.
 __device__ __forceinline__ float score_factor(float k_scale, float row) { return fmaf(k_scale, row, 0x1p-126f); }
 
 constexpr float kPagedGrow = 8.f;   // the offset moves when a term is past 2^8 of it
@@ -261,10 +269,10 @@ __device__ __forceinline__ void paged_store(const PagedParams& p, int share, lon
   }
 }
 
-// Merge of a cluster's `active` first blocks (the others have left), each of which has its rows' maxima, sums and
-// output (not divided) in its shared memory: the blocks share out the output's elements
-// and read one another's memory.  The S::MERGE_THREADS first threads of every block call it; others pass the cluster's
-// barrier as often.
+// Merge of a cluster's `active` first blocks (the others have left), each of which has its rows'
+// maxima, sums and output (not divided) in its shared memory: the blocks share out the output's
+// elements and read one another's memory.  The S::MERGE_THREADS first threads of every block call
+// it; others pass the cluster's barrier as often.
 template <typename S, typename Place>
 __device__ __forceinline__ void paged_cluster_merge(const PagedParams& p, uint8_t* smem, uint32_t sbase, int share,
                                                     int rank, int active, int nrows, long long all_rows,
@@ -362,7 +370,8 @@ __global__ void __launch_bounds__(S::THREADS, S::MIN_BLOCKS)
       for (int n = threadIdx.x; n < nrows; n += S::THREADS) p.lse_part[share * all_rows + place(n)] = -INFINITY;
     if (p.cluster == 1 || rank > 0) return;
   }
-  // blocks of the cluster that have keys: shares of a chunk each, from the first on (and the last takes the rest)
+  // blocks of the cluster that have keys: shares of a chunk each, from the first on (and the last
+  // takes the rest)
   const long long shares_used = (static_cast<long long>(lim_max) + p.chunk - 1) / p.chunk;
   const int active = p.cluster == 1 ? 1 : max(1, static_cast<int>(min(shares_used, static_cast<long long>(p.cluster))));
 
@@ -425,8 +434,8 @@ __global__ void __launch_bounds__(S::THREADS, S::MIN_BLOCKS)
   else lane_at = ((lane >> 3) & 1) * (S::BN * 128) + (lane >> 4) * 128 + (((lane & 7) ^ (lane >> 4)) << 4);
   // Copies and scales of this warp's part of stage j, whose pages are in pg.
   auto fill = [&](int j, int slot) {
-    // (a test hook: this stage never fills.  Where the warps fill their own parts it only lacks an arrival, which their
-    // loop does not notice: returning here costs it 1.5 %)
+    // (a test hook: this stage never fills.  Where the warps fill their own parts it only lacks an
+    // arrival, which their loop does not notice: returning here costs it 1.5 %)
     if (!S::SELF && j == p.drop_load) return;
     const unsigned hidden = __ballot_sync(0xffffffffu, lane < S::GROUPS && pg == -2);
     if constexpr (S::SELF) {

@@ -13,19 +13,20 @@
 //   softmax       one warpgroup a tile, one thread a row, as attn_fwd_kernel; the first
 //                 thing it does is to lay out its Q rows.
 //
-// K is multiplied as it is stored (kind::f8f6f4): a row of Q, its largest element brought to [2^7, 2^8) by a
-// power of two, is the sum of an e4m3 row and an e5m2 row, and the two products cost what one of 16 bits does.
-// e4m3 takes the upper four of bf16's eight digits; what rounding to them leaves is at most 8 of bf16's steps, which
-// e5m2's three digits hold.  So elements of 2^-6 and more are exact (2^-14 of the row's largest).  Below, e4m3's
-// step is 2^-9 and leaves up to 2^-10, where e5m2's is 2^-13: off by 2^-14 at most, 2^-21 of the row's largest.
-// (With e4m3 for the second part as well, its range would end 2^-17 below.)  P has no such range -- a flat tail
-// behind one heavy key is 2^-20 of it -- so P V is fp16 and V is converted: K's
-// conversion would cost as much again of the shared memory's time.
+// K is multiplied as it is stored (kind::f8f6f4): a row of Q, its largest element brought to [2^7,
+// 2^8) by a power of two, is the sum of an e4m3 row and an e5m2 row, and the two products cost what
+// one of 16 bits does. e4m3 takes the upper four of bf16's eight digits; what rounding to them
+// leaves is at most 8 of bf16's steps, which e5m2's three digits hold.  So elements of 2^-6 and
+// more are exact (2^-13 of the row's largest and more).  Below, e4m3's step is 2^-9 and leaves up to 2^-10,
+// where e5m2's is 2^-13: off by 2^-14 at most, 2^-21 of the row's largest. (With e4m3 for the
+// second part as well, its range would end 2^-17 below.)  P has no such range -- a flat tail behind
+// one heavy key is 2^-20 of it -- so P V is fp16 and V is converted: K's conversion would cost as
+// much again of the shared memory's time.  (P's rounding: see paged_kernel.cuh.)
 //
 // Measured (32/8 heads of 128, pages of 64): a block takes 1.75 us for 128 keys and 10 to begin
-// and end; 2 x 2048 queries against 16384 keys 775 to 840 us (1330 to 1230 TFLOP/s of 4 d flops a
-// key and row; more where scales that differ from page to page move the offset more often), 4096 against 4096
-// 137.  Of a block's beginning and end a clock showed, in cycles: sequence and lengths 1250,
+// and end; 2 x 2048 queries against 16384 keys 833 us (1240 TFLOP/s of 4 d flops a
+// key and row; less where scales that differ from page to page move the offset more often), 4096 against 4096
+// 144.  Of a block's beginning and end a clock showed, in cycles: sequence and lengths 1250,
 // barriers and tensor memory 1200, Q read and laid out 5400, the first scores 1700, a tile's softmax
 // 2250, the output 4800.  Two tiles of 128 rows take turns on the tensor cores, which ncu has busy for
 // 55 % of the time: the rest is the softmax's chain, as in attn_fwd_kernel.
@@ -165,8 +166,8 @@ __device__ __forceinline__ bool prefill_tile(const PagedParams& p, PrefillTile<S
   const int last = min(t.row0 + S::ROWS, t.rows) - 1;
   const int lim_max = paged_limit(p, t.seq, last / p.group);
   t.lim_min = paged_limit(p, t.seq, t.row0 / p.group);
-  // A cluster's blocks hold a multiprocessor each until its last one is done: they share out the keys that these rows
-  // see.  (Shares of a workspace are the same for all rows.)
+  // A cluster's blocks hold a multiprocessor each until its last one is done: they share out the
+  // keys that these rows see.  (Shares of a workspace are the same for all rows.)
   const int chunk = t.cluster > 1 ? max(1, (lim_max + S::BN * t.cluster - 1) / (S::BN * t.cluster)) * S::BN : p.chunk;
   const long long first = static_cast<long long>(t.split) * chunk;
   const int t_begin = static_cast<int>(min(first, static_cast<long long>(lim_max)));
@@ -501,9 +502,6 @@ __device__ __forceinline__ float prefill_max(const uint32_t (&s)[NCH][32], float
   return m;
 }
 
-// A warp's 32 rows as it reads and writes them: a row is in LANES lanes of 16 bytes of bf16, and the I-th access has
-// rows I * ROWS to (I + 1) * ROWS - 1.  (A row a thread touches 32 lines an access: with that a block of 128 keys, d =
-// 128, took 14.2 us from its launch to the next one's, 11.6 this way.)
 __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
@@ -520,6 +518,10 @@ __device__ __forceinline__ uint32_t pack_e5m2x4(float b0, float b1, float b2, fl
   return r;
 }
 
+// A warp's 32 rows as it reads and writes them: a row is in LANES lanes of 16 bytes of bf16, and
+// the I-th access has rows I * ROWS to (I + 1) * ROWS - 1.  (A row a thread touches 32 lines an
+// access: with that a block of 128 keys, d = 128, took 14.2 us from its launch to the next one's,
+// 11.6 this way.)
 template <typename S>
 struct PrefillRows {
   static constexpr int LANES = S::D / 8, ROWS = 32 / LANES, ACCESSES = LANES;
@@ -551,8 +553,8 @@ __device__ __forceinline__ void prefill_fetch(int q, const PagedParams& p, const
   }
 }
 
-// Lays out a warp's rows of Q, each with its largest element brought to [2^7, 2^8), as an e4m3 and an e5m2 row, and
-// returns the factor of this thread's row's scores.
+// Lays out a warp's rows of Q, each with its largest element brought to [2^7, 2^8), as an e4m3 and
+// an e5m2 row, and returns the factor of this thread's row's scores.
 template <typename S>
 __device__ __forceinline__ float prefill_lay_out(int q, uint32_t sbase, const PagedParams& p, const PrefillQ<S>& in) {
   using A = PrefillRows<S>;
@@ -583,7 +585,8 @@ __device__ __forceinline__ float prefill_lay_out(int q, uint32_t sbase, const Pa
 #pragma unroll
   for (int i = 0; i < A::ACCESSES; ++i) {
     const uint32_t u[4] = {in.v[i].x, in.v[i].y, in.v[i].z, in.v[i].w};
-    // a row with an infinity or NaN is NaN throughout, so that every score of it is, and a masked one stays masked
+    // a row with an infinity or NaN is NaN throughout, so that every score of it is, and a masked
+    // one stays masked
     const float down =
         top[i] >= 0x7f80u ? NAN : __uint_as_float(static_cast<unsigned>(127 - exponent(top[i])) << 23) * 0x1p7f;
     uint32_t hi[2], lo[2];
@@ -805,7 +808,7 @@ __device__ PrefillRow<S> prefill_softmax(int q, uint32_t tmem, uint8_t* smem, ui
   return out;
 }
 
-// Four chunks of 32 elements at most of a row's output, times `factor`, to use(chunk, values).
+// A row's output times `factor`, 32 elements at a time, to use(chunk, values).
 template <typename S, typename Use>
 __device__ __forceinline__ void prefill_output(int q, uint32_t tmem, const PrefillRow<S>& row, float factor, Use&& use) {
   const uint32_t o_t = tmem + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) * 32 << 16) + S::o_col(q);
@@ -872,7 +875,8 @@ __device__ __forceinline__ void prefill_store(int q, uint32_t tmem, uint32_t sba
   }
 }
 
-// The row's part to this block's shared memory, for the cluster's merge; every role is done with the tiles there.
+// The row's part to this block's shared memory, for the cluster's merge; every role is done with
+// the tiles there.
 template <typename S>
 __device__ __forceinline__ void prefill_offer(int q, uint32_t tmem, uint8_t* smem, const PrefillRow<S>& row) {
   const int n = q * BM + (threadIdx.x & 127);
@@ -900,9 +904,10 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   if (!prefill_tile<S>(p, t, threadIdx.x == 0)) return;
   volatile uint32_t* abort_flag = reinterpret_cast<volatile uint32_t*>(smem + S::OFF_ABORT);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::OFF_TMEMSLOT);
-  // The warps that wait for copies have the caller's limit.  The softmax, which the abort flag stops, has the usual one as a
-  // constant: its loop takes up to 7 % longer or shorter by what else the compiler keeps in its registers (2 x 2048
-  // queries against 16384 keys, d = 128: 837 us so, 890 with the limit from the parameters).
+  // The warps that wait for copies have the caller's limit.  The softmax, which the abort flag
+  // stops, has the usual one as a constant: its loop takes up to 7 % longer or shorter by what else
+  // the compiler keeps in its registers (2 x 2048 queries against 16384 keys, d = 128: 837 us so,
+  // 890 with the limit from the parameters).
   const Waiter w{abort_flag, p.status, p.wait_timeout_ns}, w_softmax{abort_flag, p.status};
   // for the epilogue, so that the softmax does not keep it in registers where those are short
   static_assert(sizeof(PrefillTile<S>) <= 96, "the tile's place");
@@ -922,7 +927,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
     prefetch_tensormap(&tm_k);
     prefetch_tensormap(&tm_v);
   }
-  // The block's barriers and tensor memory are there; what a role can load without them is on its way by then.
+  // The block's barriers and tensor memory are there; what a role can load without them is on its
+  // way by then.
   auto begin = [&] {
     tc_fence_before_sync();
     __syncthreads();
@@ -932,7 +938,8 @@ __global__ void __launch_bounds__(S::THREADS, 1)
   if (warp < 4 * S::NQ) {
     const int q = warp >> 2;
     PrefillQ<S> rows;
-    // (measured at d = 64 and 128, a block of 128 keys: 8.2 and 11.5 us before begin(), 8.3 and 11.0 behind it)
+    // (measured at d = 64 and 128, a block of 128 keys: 8.2 and 11.5 us before begin(), 8.3 and
+    // 11.0 behind it)
     if constexpr (S::D == 64) prefill_fetch<S>(q, p, t, rows);
     const uint32_t tmem = begin();
     if constexpr (S::SPLIT_REGS) setmaxnreg_inc<S::REG_SOFTMAX>();

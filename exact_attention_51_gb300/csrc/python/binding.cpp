@@ -74,8 +74,9 @@ bool truth(PyObject* o) {
 
 // The stream of a call: the given one, or torch's current one on the device.
 //
-// What the call allocates is of the call's stream: torch's allocator hands out a freed block again in the order of
-// the stream that it is of, so that on any other one the kernels before could still be using it.
+// What the call allocates is of the call's stream: torch's allocator hands out a freed block again
+// in the order of the stream that it is of, so that on any other one the kernels before could still
+// be using it.
 struct Stream {
   void* handle;
   c10::cuda::CUDAStream current;  // the caller's
@@ -140,8 +141,9 @@ at::Tensor new_like(const at::Tensor& x) {
   return new_tensor(x.sizes(), x.scalar_type(), x.device());
 }
 
-// Counts a write into a tensor of the caller's, as torch's in-place operations do: autograd then refuses a value
-// that it saved and that has changed since.  (Inference tensors have no count, and autograd saves none.)
+// Counts a write into a tensor of the caller's, as torch's in-place operations do: autograd then
+// refuses a value that it saved and that has changed since.  (Inference tensors have no count, and
+// autograd saves none.)
 void written(const at::Tensor& t) {
   if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
@@ -270,7 +272,8 @@ const at::Tensor& bf16_rows(PyObject* o, const char* name) {
   return *t;
 }
 
-// append(k, v, slots, k_cache, v_cache, k_scale, v_scale, phases, positions, interleaved, attention_factor, stream)
+// append(k, v, slots, k_cache, v_cache, k_scale, v_scale, phases, positions, interleaved,
+// attention_factor, stream)
 PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     if (n != 12) type_error("append takes 12 arguments");
@@ -309,7 +312,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// paged(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_start, max_q, max_kv, causal, scale, num_splits,
+// paged(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_start, max_q, max_kv, causal,
+// scale, num_splits,
 //       out, lse, workspace, stream)
 PyObject* paged(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {

@@ -11,7 +11,10 @@
  * 2^-60 to 2^60, the ones that attn_paged_append_fp8 writes: a block whose
  * scale has to grow then keeps its codes exactly (but for those that leave the
  * type's normal range), however often it grows.  attn_fwd_fp8_paged reads
- * scales of any other value in that range too.
+ * scales of any other value in that range too.  Of a sequence and head it wants
+ * V's scales within 2^100 of each other: a key whose weight times V scale is
+ * less than 2^-133 of the largest such product is left out, which within that
+ * spread is no weight above 2^-33 of the largest.
  *
  * A sequence's tokens lie in the pages that its row of the page table names:
  * token j is token j % page_size of page block_table[b][j / page_size].
@@ -90,7 +93,8 @@ ATTN_API int attn_paged_append_fp8(const void* k, const void* v, int T, int Hkv,
  *              0 is allowed (less counts as 0).
  *   block_table  device int32 [B, table_stride]: page numbers; entries from
  *              ceil(kv_len / page_size) on are not used.
- *   max_q      no sequence has more query tokens (1 for decoding).
+ *   max_q      no sequence has more query tokens (1 for decoding; a larger one
+ *              than need be costs time, as it picks the kernel and its tiles).
  *   max_kv     about the longest kv_len: only the sharing out of the keys goes by it,
  *              and the result does not depend on it.
  *   causal     query i of n sees keys j <= i + kv_len - n (the queries are the
@@ -104,6 +108,11 @@ ATTN_API int attn_paged_append_fp8(const void* k, const void* v, int T, int Hkv,
  *   workspace  attn_fwd_fp8_paged_workspace_size(T, Hq, Hkv, d, max_q, num_splits) bytes,
  *              256-byte aligned; NULL where that is 0.  Scratch until the call's last
  *              kernel has run: calls that may overlap need one each.
+ *
+ * Scores are fp32 sums of exact products of the codes and Q, whose elements are
+ * held to 2^-25 (up to 16 rows) or 2^-21 (more) of their row's largest, exactly
+ * from 2^-13 of it on; a weight is rounded to fp16 (2^-11 of itself) where it
+ * meets V, and O once to bf16.
  *
  * Masked keys do not reach the result, whatever their codes (NaN among them)
  * and scales.  Codes of tokens from kv_len on are never used.
@@ -139,12 +148,13 @@ ATTN_API int attn_fwd_fp8_paged_num_splits(int B, int Hq, int Hkv, int d, int pa
  * Self-test of the kernels' own abort path (a test hook, not a way to compute
  * attention), as attn_selftest_fwd_dropped_load: attn_fwd_fp8_paged on the given
  * arguments, except that every thread block leaves out one load and every wait gives
- * up after `timeout_ms` (1..10000) milliseconds.  drop_load >= 0: up to 16 rows, the ring's stage of
- * that number (128 keys each, 64 at d = 256 in pages of 16); more rows, 2 j for the keys and 2 j + 1 for the values of the
- * block's key tile j (128 keys, 64 at d = 256).  Blocks with fewer run to the end.  O and LSE are
- * not valid afterwards; attn_fwd_device_status returns ATTN_ERR_TIMEOUT with the code of the
- * wait that gave up first (0x14x up to 16 rows, 0x15x more) and clears the word.  Run it only when
- * no other launch of the library is in flight on the device.
+ * up after `timeout_ms` (1..10000) milliseconds.  drop_load >= 0: up to 16 rows,
+ * the ring's stage of that number (128 keys each, 64 at d = 256); more rows, 2 j
+ * for the keys and 2 j + 1 for the values of the block's key tile j (128 keys, 64
+ * at d = 256).  Blocks with fewer run to the end.  O and LSE are not valid
+ * afterwards; attn_fwd_device_status returns ATTN_ERR_TIMEOUT with the code of the
+ * wait that gave up first (0x14x up to 16 rows, 0x15x more) and clears the word.
+ * Run it only when no other launch of the library is in flight on the device.
  */
 ATTN_API int attn_selftest_fwd_fp8_paged_dropped_load(
     const void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k_cache, const void* v_cache,

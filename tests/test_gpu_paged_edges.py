@@ -101,6 +101,18 @@ def test_rows_of_q_with_one_large_element(new, d):
         assert_close(ea.attn_fwd_fp8_paged(**dev, max_q=new, max_kv=90, scale=scale, num_splits=splits), (o, lse, tol_o, tol_l))
 
 
+@pytest.mark.parametrize("new", [3, 70])
+def test_scales_of_v_a_hundred_powers_apart(new):
+    """Blocks of V of 2^-50 to 2^50: the weights of the small ones count all the same."""
+    g = torch.Generator().manual_seed(66)
+    c = case([300, 90], [1, new], 4, 2, 64, 16, seed=66, spread=0)
+    c["vs"] = 2.0 ** torch.randint(0, 2, c["vs"].shape, generator=g).float().mul(100).sub(50)
+    want = reference(c, scale=0.5)
+    dev = on_gpu(c)
+    for splits in (1, 2, 9):
+        assert_close(ea.attn_fwd_fp8_paged(**dev, max_q=new, max_kv=300, scale=0.5, num_splits=splits), want)
+
+
 @pytest.mark.parametrize("d,tokens", [(64, 270), (128, 270), (256, 134)])
 def test_last_wave_sees_what_was_written_right_before(d, tokens):
     """A wave of blocks and a few more, whose keys pairs of blocks share: lengths, page

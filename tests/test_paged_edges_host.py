@@ -77,9 +77,9 @@ PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459")
 @pytest.mark.parametrize("rot,base", [(2, 10000.0), (64, 10000.0), (128, 1e6), (512, 1.5), (96, 500000.0)])
 @pytest.mark.parametrize("scaling,factor", [("none", 1.0), ("linear", 8.0), ("ntk", 4.0)])
 def test_phases_within_a_fraction_of_a_turn(rot, base, scaling, factor):
-    """f / 2 pi to 2^-52 of a turn.  fp64 rounds by 2^-53: pow's result twice, the exponent, which f e ln(base) of
-    passes on (at most 1 / e of a turn's 2 pi-th), 2 pi, the division and the scaling, NTK's base with three of its own:
-    some 2^-50.4 of f / 2 pi, which is 0.16 at most: 2^-53."""
+    """f / 2 pi = base^-e / 2 pi to 2^-52 of a turn, in steps of fp64 (2^-53 of the value each): pow's
+    result, 2; 2 pi, the division and the scaling, 3; and as errors of the exponent and of
+    NTK's base (3) reach f times e ln(base) and e, at most 1 / e and 1 of f, 4 more: 9 steps of 0.16 at most."""
     if scaling == "ntk" and rot == 2:
         return
     getcontext().prec = 40
