@@ -434,9 +434,6 @@ __global__ void __launch_bounds__(S::THREADS, S::MIN_BLOCKS)
   else lane_at = ((lane >> 3) & 1) * (S::BN * 128) + (lane >> 4) * 128 + (((lane & 7) ^ (lane >> 4)) << 4);
   // Copies and scales of this warp's part of stage j, whose pages are in pg.
   auto fill = [&](int j, int slot) {
-    // (a test hook: this stage never fills.  Where the warps fill their own parts it only lacks an
-    // arrival, which their loop does not notice: returning here costs it 1.5 %)
-    if (!S::SELF && j == p.drop_load) return;
     const unsigned hidden = __ballot_sync(0xffffffffu, lane < S::GROUPS && pg == -2);
     if constexpr (S::SELF) {
 #pragma unroll
@@ -484,7 +481,9 @@ __global__ void __launch_bounds__(S::THREADS, S::MIN_BLOCKS)
     }
     if (lane == 0) reinterpret_cast<unsigned*>(m)[32 + (S::SELF ? warp : 0)] = hidden;
     __syncwarp();
-    if (lane == 0 && (!S::SELF || j != p.drop_load)) mbar_arrive(full(slot));
+    // (a test hook: the stage that lacks this arrival never fills.  Leaving its copies out as well
+    // would cost calls without the hook 2 %: 24 ragged sequences at d = 256 25.2 us for 24.7)
+    if (lane == 0 && j != p.drop_load) mbar_arrive(full(slot));
   };
   // What the fill after stage j uses is on its way until then.
   auto advance = [&](int j) {
@@ -610,7 +609,8 @@ __global__ void __launch_bounds__(S::THREADS, S::MIN_BLOCKS)
       advance(filled);
       if (++st == STAGES) st = 0, phase ^= 1u;
     }
-    // no copy is in flight when the block ends, whoever's wait gives up before the stage is used
+    // No copy is in flight when the block ends, whoever's wait gives up before the stage is used.
+    // (A stage that a test leaves unfilled has its copies behind it by the time that a wait for it gives up.)
     for (int i = max(0, filled - STAGES); i < filled; ++i)
       if (i != p.drop_load) drain_phase(full(i % STAGES), static_cast<uint32_t>(i / STAGES) & 1u, w, kCodeDrain);
     __syncwarp();

@@ -147,7 +147,7 @@ ATTN_API int attn_fwd_fp8_paged_num_splits(int B, int Hq, int Hkv, int d, int pa
 /*
  * Self-test of the kernels' own abort path (a test hook, not a way to compute
  * attention), as attn_selftest_fwd_dropped_load: attn_fwd_fp8_paged on the given
- * arguments, except that every thread block leaves out one load and every wait gives
+ * arguments, except that one load never arrives in any thread block and every wait gives
  * up after `timeout_ms` (1..10000) milliseconds.  drop_load >= 0: up to 16 rows,
  * the ring's stage of that number (128 keys each, 64 at d = 256); more rows, 2 j
  * for the keys and 2 j + 1 for the values of the block's key tile j (128 keys, 64
