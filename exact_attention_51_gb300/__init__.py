@@ -534,8 +534,20 @@ def attn_selftest_fwd_fp8_paged_dropped_load(q, k_cache, v_cache, k_scale, v_sca
     left out and every wait limited to ``timeout_ms``.  Returns the C status; the
     outcome is read with ``attn_fwd_device_status``."""
     import torch
+    if any(t.dtype not in (torch.float8_e4m3fn, torch.uint8) for t in (k_cache, v_cache)) \
+            or any(t.dtype != torch.float32 for t in (k_scale, v_scale)) \
+            or any(t.dtype != torch.int32 for t in (block_table, kv_len, q_start)) \
+            or q.dtype != torch.bfloat16:
+        raise TypeError("q must be bf16, the codes e4m3, the scales fp32, the indexes int32")
+    rest = (k_cache, v_cache, k_scale, v_scale, block_table, kv_len, q_start)
+    if not q.is_cuda or q.stride(-1) != 1 \
+            or any(t.device != q.device or not t.is_contiguous() for t in rest):
+        raise ValueError("contiguous tensors on one CUDA device are wanted")
     T, Hq, d = q.shape
     Hkv, (B, width) = k_cache.shape[1], block_table.shape
+    if v_cache.shape != k_cache.shape or k_cache.shape[3] != d or kv_len.shape != (B,) \
+            or q_start.shape != (B + 1,) or any(s.shape != k_cache.shape[:2] for s in (k_scale, v_scale)):
+        raise ValueError("the shapes must be those of attn_fwd_fp8_paged")
     out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=q.device)
     lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
     need = attn_fwd_fp8_paged_workspace_size(T, Hq, Hkv, d, max_q, num_splits)

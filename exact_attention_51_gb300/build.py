@@ -97,7 +97,11 @@ def _binding_stamp() -> str | None:
     spec = importlib.util.find_spec("torch")
     if spec is None:
         return None
-    return "\n".join([f"torch {importlib.metadata.version('torch')}", str(spec.origin),
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:  # (run from a source tree)
+        version = "of no package"
+    return "\n".join([f"torch {version}", str(spec.origin),
                       str(sysconfig.get_config_var("SOABI"))])
 
 

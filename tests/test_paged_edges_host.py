@@ -90,3 +90,13 @@ def test_phases_within_a_fraction_of_a_turn(rot, base, scaling, factor):
     for i, u in enumerate(got.tolist()):
         f = (b.ln() * Decimal(-2 * i) / rot).exp() / (Decimal(factor) if scaling == "linear" else 1)
         assert abs(Decimal(u) / 2 ** 64 - f / (2 * PI)) <= Decimal(2) ** -52
+
+
+def test_paged_selftest_refuses_what_the_gpu_cannot_read():
+    c, s, i = torch.zeros((2, 1, 16, 64), dtype=torch.uint8), torch.zeros((2, 1)), torch.zeros(2, dtype=torch.int32)
+    q = torch.zeros((1, 1, 64), dtype=torch.bfloat16)
+    rest = dict(max_q=1, max_kv=16, num_splits=1, drop_load=0)
+    with pytest.raises(ValueError):
+        ea.attn_selftest_fwd_fp8_paged_dropped_load(q, c, c, s, s, i[None], i[:1], i, **rest)
+    with pytest.raises(TypeError):
+        ea.attn_selftest_fwd_fp8_paged_dropped_load(q.float(), c, c, s, s, i[None], i[:1], i, **rest)
